@@ -6,7 +6,8 @@ ABI in include/moe.h (moe_route, moe_dispatch, moe_quantize_act,
 moe_forward, moe_forward_fused, moe_forward_fused_status, moe_route_forward,
 moe_forward_noalloc, moe_cap_swiglu, moe_workspace_size,
 moe_noalloc_scratch_bytes, moe_check_arch, moe_status_string, the weight
-encoder and decoder).
+encoder and decoder, moe_group_product, moe_route_logits, and the router's
+balance loss with its gradient).
 Tensors must be contiguous and on the current CUDA (HIP) device; apart from
 moe_forward_noalloc's fixed device array the library never allocates, so
 callers pass outputs and a workspace.
@@ -22,8 +23,8 @@ from dataclasses import dataclass
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("BSE_MOE_LIB") or os.path.join(HERE, "libmoe.so")
 
-FMT_NVFP4, FMT_MXFP8 = 1, 2
-FMTS = {"nvfp4": FMT_NVFP4, "mxfp8": FMT_MXFP8}
+FMT_NVFP4, FMT_MXFP8, FMT_MXFP4 = 1, 2, 4
+FMTS = {"nvfp4": FMT_NVFP4, "mxfp8": FMT_MXFP8, "mxfp4": FMT_MXFP4}
 CAP_SOFT_GATE_UP, CAP_HARD_GATE_UP, CAP_SOFT_OUT, CAP_NONE = 0, 1, 2, 3
 DTYPE_BF16, DTYPE_F32 = 0, 1
 ACT_GS_PER_ROW, ACT_GS_PER_TENSOR, ACT_GS_STATIC = 0, 1, 2
@@ -33,7 +34,9 @@ STAGES = ("quant_x", "dispatch", "gate_up", "quant_h", "down", "combine")
 EXPORTED = ("moe_status_string", "moe_check_arch", "moe_validate_config", "moe_workspace_size",
             "moe_quantize_act", "moe_route", "moe_dispatch", "moe_prepare_weights", "moe_forward",
             "moe_forward_fused", "moe_forward_fused_status", "moe_cap_swiglu", "moe_encode_weights",
-            "moe_decode_weights", "moe_forward_noalloc", "moe_noalloc_scratch_bytes", "moe_route_forward")
+            "moe_decode_weights", "moe_forward_noalloc", "moe_noalloc_scratch_bytes", "moe_route_forward",
+            "moe_route_logits", "moe_balance_workspace_size", "moe_balance_forward", "moe_balance_backward",
+            "moe_group_product")
 LAYOUT_CANONICAL, LAYOUT_PACKED = 0, 1
 
 
@@ -89,6 +92,13 @@ def load() -> ctypes.CDLL:
     lib.moe_noalloc_scratch_bytes.argtypes = []
     lib.moe_route_forward.argtypes = [ctypes.POINTER(CConfig), vp, i32, vp, vp, vp, vp, vp, ctypes.POINTER(CWeights),
                                       vp, vp, sz, vp, vp]
+    lib.moe_route_logits.argtypes = [ctypes.POINTER(CConfig), i32, vp, sz, vp, vp]
+    lib.moe_balance_workspace_size.argtypes = [ctypes.POINTER(CConfig), i32, i32, ctypes.POINTER(sz)]
+    lib.moe_balance_forward.argtypes = [ctypes.POINTER(CConfig), i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+                                        sz, vp]
+    lib.moe_balance_backward.argtypes = [ctypes.POINTER(CConfig), i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+                                         vp]
+    lib.moe_group_product.argtypes = [i32, vp, vp, i32, vp, i32, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp]
     for name in EXPORTED:
         if name != "moe_status_string":
             getattr(lib, name).restype = ctypes.c_int
@@ -158,6 +168,16 @@ def _ptr(t, dtype=None, shape=None, name="tensor"):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _code_cols(fmt: str, cols: int) -> int:
+    """Bytes of a row of `cols` codes."""
+    return cols if fmt == "mxfp8" else cols // 2
+
+
+def _scale_cols(fmt: str, cols: int) -> int:
+    """Scales of a row of `cols` elements."""
+    return cols // (16 if fmt == "nvfp4" else 32)
+
+
 def workspace_size(cfg: Config) -> int:
     n = ctypes.c_size_t(0)
     cc = cfg.c()
@@ -171,7 +191,7 @@ def workspace(cfg: Config, device="cuda"):
 
 
 def quantize_act(cfg, x, codes, scales, row_gs=None, site: int = 0, ws=None) -> None:
-    """NVFP4 / MXFP8 quantization of a bf16 or fp32 [rows, cols] tensor in
+    """NVFP4 / MXFP8 / MXFP4 quantization of a bf16 or fp32 [rows, cols] tensor in
     cfg's format and activation-scale mode (cfg: a Config, or a format name
     for the per-row default).  site 0: gate/up input x, 1: down input h.
     ws: uint8 scratch of at least ACT_GS_SCRATCH_BYTES for NVFP4 per-tensor
@@ -187,8 +207,8 @@ def quantize_act(cfg, x, codes, scales, row_gs=None, site: int = 0, ws=None) -> 
     _ptr(x, name="x")
     cc = cfg.c()
     args = (ctypes.byref(cc), site, dt, _ptr(x), rows, cols,
-            _ptr(codes, torch.uint8, (rows, cols // 2 if nv else cols), "codes"),
-            _ptr(scales, torch.uint8, (rows, cols // (16 if nv else 32)), "scales"),
+            _ptr(codes, torch.uint8, (rows, _code_cols(cfg.fmt, cols)), "codes"),
+            _ptr(scales, torch.uint8, (rows, _scale_cols(cfg.fmt, cols)), "scales"),
             _ptr(row_gs, torch.float32, (rows,), "row_gs") if nv else None,
             _ptr(ws, torch.uint8, None, "ws"), 0 if ws is None else ws.numel(), _stream())
     _ok(load().moe_quantize_act(*args), "moe_quantize_act")
@@ -227,8 +247,8 @@ def encode_weights(fmt: str, w, codes, scales, gs=None, gs_group: int = 1, gs_st
     """Matrices w [nmat, rows, cols] (bf16 or fp32) to NVFP4 (one fp32 scale
     per matrix, recomputed from its max |w|, written to gs[(m // gs_group) *
     gs_stride + m % gs_group]; ws: int32 scratch of at least nmat elements)
-    or MXFP8.  codes / scales: uint8 [nmat, rows, cols/2 or cols] and
-    [nmat, rows, cols/16 or cols/32]."""
+    or MXFP8 / MXFP4.  codes / scales: uint8 [nmat, rows, cols/2 (MXFP8: cols)]
+    and [nmat, rows, cols/32 (NVFP4: cols/16)]."""
     import torch
     nmat, rows, cols = w.shape
     dt = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(w.dtype)
@@ -241,8 +261,8 @@ def encode_weights(fmt: str, w, codes, scales, gs=None, gs_group: int = 1, gs_st
         if ws is None or ws.numel() < nmat:
             raise ValueError(f"ws must hold at least {nmat} int32")
     args = (FMTS[fmt], dt, _ptr(w), nmat, rows, cols,
-            _ptr(codes, torch.uint8, (nmat, rows, cols // 2 if nv else cols), "codes"),
-            _ptr(scales, torch.uint8, (nmat, rows, cols // (16 if nv else 32)), "scales"),
+            _ptr(codes, torch.uint8, (nmat, rows, _code_cols(fmt, cols)), "codes"),
+            _ptr(scales, torch.uint8, (nmat, rows, _scale_cols(fmt, cols)), "scales"),
             _ptr(gs, torch.float32, None, "gs") if nv else None, gs_group, gs_stride,
             _ptr(ws, torch.int32, None, "ws") if nv else None,
             (ws.numel() * 4) if (nv and ws is not None) else 0, _stream())
@@ -256,8 +276,8 @@ def decode_weights(fmt: str, codes, scales, out, gs=None, gs_group: int = 1, gs_
     nv = fmt == "nvfp4"
     if nv:
         _check_gs(gs, nmat, gs_group, gs_stride)
-    args = (FMTS[fmt], _ptr(codes, torch.uint8, (nmat, rows, cols // 2 if nv else cols), "codes"),
-            _ptr(scales, torch.uint8, (nmat, rows, cols // (16 if nv else 32)), "scales"),
+    args = (FMTS[fmt], _ptr(codes, torch.uint8, (nmat, rows, _code_cols(fmt, cols)), "codes"),
+            _ptr(scales, torch.uint8, (nmat, rows, _scale_cols(fmt, cols)), "scales"),
             _ptr(gs, torch.float32, None, "gs") if nv else None, gs_group, gs_stride, nmat, rows, cols,
             _ptr(out, torch.float32, None, "out"), _stream())
     _ok(load().moe_decode_weights(*args), "moe_decode_weights")
@@ -275,6 +295,99 @@ def route(cfg: Config, x, w_router, bias, topk_ids, topk_w, near_tie, ws) -> Non
                          _ptr(topk_w, torch.float32, (T, k), "topk_w"),
                          _ptr(near_tie, torch.uint8, (T,), "near_tie"),
                          _ptr(ws, torch.uint8, None, "ws"), ws.numel(), _stream()), "moe_route")
+
+
+def route_logits(cfg: Config, T: int, z, ws) -> None:
+    """z [T, E] fp32 <- the logits the last route / route_forward of T tokens
+    on ws selected from."""
+    import torch
+    cc = cfg.c()
+    _ok(load().moe_route_logits(ctypes.byref(cc), T, _ptr(ws, torch.uint8, None, "ws"), ws.numel(),
+                                _ptr(z, torch.float32, (T, cfg.num_experts), "z"), _stream()), "moe_route_logits")
+
+
+def balance_workspace_size(cfg: Config, T: int, S: int = 1) -> int:
+    n = ctypes.c_size_t(0)
+    cc = cfg.c()
+    _ok(load().moe_balance_workspace_size(ctypes.byref(cc), T, S, ctypes.byref(n)), "moe_balance_workspace_size")
+    return n.value
+
+
+def balance_workspace(cfg: Config, T: int, S: int = 1, device="cuda"):
+    import torch
+    return torch.empty(balance_workspace_size(cfg, T, S), dtype=torch.uint8, device=device)
+
+
+def _balance_args(cfg: Config, z, topk_ids, seq_offsets, token_mask):
+    """Pointers shared by the two balance calls: (dtype, z, T, ids, seq_offsets, S, mask)."""
+    import torch
+    dt = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(z.dtype)
+    if dt is None:
+        raise ValueError("z must be bfloat16 or float32")
+    T = z.shape[0]
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    return (dt, _ptr(z, None, (T, cfg.num_experts), "z"), T,
+            _ptr(topk_ids, torch.int32, (T, cfg.top_k), "topk_ids"),
+            _ptr(seq_offsets, torch.int32, (S + 1,), "seq_offsets"), S,
+            _ptr(token_mask, torch.uint8, (T,), "token_mask"))
+
+
+def balance_forward(cfg: Config, z, topk_ids, counts, live, probs, loss, ws, seq_offsets=None,
+                    token_mask=None) -> None:
+    """Per-expert counts [S, E] (int32), live tokens [S] (int32), mean
+    probabilities [S, E] and balance loss [S] (fp32) of each sequence from the
+    router logits z [T, E] (bf16 or fp32) and topk_ids.  seq_offsets: int32
+    [S + 1] (None: one sequence); token_mask: uint8 [T], 0 = not a token.
+    ws: balance_workspace(cfg, T, S)."""
+    import torch
+    args = _balance_args(cfg, z, topk_ids, seq_offsets, token_mask)
+    S, E = args[5], cfg.num_experts
+    cc = cfg.c()
+    _ok(load().moe_balance_forward(ctypes.byref(cc), *args, _ptr(counts, torch.int32, (S, E), "counts"),
+                                   _ptr(live, torch.int32, (S,), "live"),
+                                   _ptr(probs, torch.float32, (S, E), "probs"),
+                                   _ptr(loss, torch.float32, (S,), "loss"), _ptr(ws, torch.uint8, None, "ws"),
+                                   ws.numel(), _stream()), "moe_balance_forward")
+
+
+def balance_backward(cfg: Config, z, topk_ids, counts, live, d_loss, dz, d_topk_w=None, seq_offsets=None,
+                     token_mask=None) -> None:
+    """dz [T, E] (z's dtype) <- the gradient of sum(d_loss * loss) and, with
+    d_topk_w [T, k] given, of the gate weights, with respect to the logits.
+    counts, live: balance_forward's."""
+    import torch
+    args = _balance_args(cfg, z, topk_ids, seq_offsets, token_mask)
+    T, S, E = args[2], args[5], cfg.num_experts
+    cc = cfg.c()
+    _ok(load().moe_balance_backward(ctypes.byref(cc), *args, _ptr(counts, torch.int32, (S, E), "counts"),
+                                    _ptr(live, torch.int32, (S,), "live"),
+                                    _ptr(d_loss, torch.float32, (S,), "d_loss"),
+                                    _ptr(d_topk_w, torch.float32, (T, cfg.top_k), "d_topk_w"),
+                                    _ptr(dz, z.dtype, (T, E), "dz"), _stream()), "moe_balance_backward")
+
+
+def group_product(fmt: str, a, a_scales, w, w_scales, offsets, out, row_ids=None, id_div: int = 1) -> None:
+    """out[r] = A[src(r)] @ W[g].T for rows r in [offsets[g], offsets[g+1]),
+    src(r) = r, or row_ids[r] // id_div.  a / a_scales: uint8 codes
+    [rows, K/2] and scales [rows, K/32]; w / w_scales: [G, N, K/2] and
+    [G, N, K/32]; offsets int32 [G+1]; out [M, N] fp32 or bf16; row_ids int32
+    [M].  fmt "mxfp4"."""
+    import torch
+    if fmt not in FMTS:
+        raise ValueError(f"unknown format {fmt!r}")
+    dt = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(out.dtype)
+    if dt is None:
+        raise ValueError("out must be bfloat16 or float32")
+    M, N = out.shape
+    G, K = w.shape[0], a.shape[1] * 2
+    a_rows = a.shape[0]
+    _ok(load().moe_group_product(FMTS[fmt], _ptr(a, torch.uint8, None, "a"),
+                                 _ptr(a_scales, torch.uint8, (a_rows, K // 32), "a_scales"), a_rows,
+                                 _ptr(row_ids, torch.int32, (M,), "row_ids"), id_div, M,
+                                 _ptr(w, torch.uint8, (G, N, K // 2), "w"),
+                                 _ptr(w_scales, torch.uint8, (G, N, K // 32), "w_scales"), G, N, K,
+                                 _ptr(offsets, torch.int32, (G + 1,), "offsets"), dt, _ptr(out, None, None, "out"),
+                                 _stream()), "moe_group_product")
 
 
 def dispatch(cfg: Config, topk_ids, expert_offsets, sorted_pairs=None, pair_pos=None, ws=None) -> None:
@@ -296,8 +409,8 @@ def weights_struct(cfg: Config, w: dict) -> CWeights:
     H, F, n = cfg.hidden, cfg.ffn, cfg.num_local
     nv = cfg.fmt == "nvfp4"
     shapes = {
-        "w13": (n, 2 * F, H // 2 if nv else H), "w13_sc": (n, 2 * F, H // (16 if nv else 32)),
-        "w2": (n, H, F // 2 if nv else F), "w2_sc": (n, H, F // (16 if nv else 32)),
+        "w13": (n, 2 * F, _code_cols(cfg.fmt, H)), "w13_sc": (n, 2 * F, _scale_cols(cfg.fmt, H)),
+        "w2": (n, H, _code_cols(cfg.fmt, F)), "w2_sc": (n, H, _scale_cols(cfg.fmt, F)),
     }
     ptrs = {k: _ptr(w[k], torch.uint8, s, k) for k, s in shapes.items()}
     gs = _ptr(w["gs"], torch.float32, (n, 3), "gs") if nv else None

@@ -44,7 +44,7 @@ Layout layout(const moe_config* c, int T) {
   Layout L;
   const size_t H = c->hidden, F = c->ffn, E = c->num_experts, EL = n_local(c), k = c->top_k;
   const size_t P = (size_t)T * k;
-  const bool nv = c->fmt == MOE_FMT_NVFP4;
+  const bool nv = c->fmt == MOE_FMT_NVFP4, mx4 = c->fmt == MOE_FMT_MXFP4;
   L.nchunks = P > 0 ? ceil_div((long)P, dispatch_chunk((int)P)) : 0;
   L.max_tiles = ceil_div((long)P, 16) + (int)EL;   // smallest tile_m is 16
   size_t o = 0;
@@ -54,7 +54,7 @@ Layout layout(const moe_config* c, int T) {
     return at;
   };
   L.z = take(router_z_rows(T) * E * 4);
-  L.xq = take((size_t)T * (nv ? H / 2 : H));
+  L.xq = take((size_t)T * (nv || mx4 ? H / 2 : H));
   L.xs = take((size_t)T * (nv ? H / 16 : H / 32));
   L.xg = take((size_t)T * 4);
   L.ags = take(nv ? kActGsScratchBytes : 0);   // NVFP4 per-tensor scale: partial maxima + the scale
@@ -67,8 +67,9 @@ Layout layout(const moe_config* c, int T) {
   L.ntiles = take(4);
   L.ctl = take((size_t)fused_ctl_words(L.max_tiles) * 4);
   L.flags = take((size_t)route_prep_flag_words((int)E) * 8);   // moe_route_forward's completion flags
-  L.h = take(nv ? P * F * 4 : 0);    // fp32 h: NVFP4 only (MXFP8 h is encoded by the gate/up epilogue)
-  L.hq = take(P * (nv ? F / 2 : F));
+  // fp32 h (NVFP4) or [gate | up] (MXFP4); MXFP8 h is encoded by the gate/up epilogue
+  L.h = take(nv ? P * F * 4 : mx4 ? P * 2 * F * 4 : 0);
+  L.hq = take(P * (nv || mx4 ? F / 2 : F));
   L.hs = take(P * (nv ? F / 16 : F / 32));
   L.hg = take(nv ? P * 4 : 0);
   L.y = take(P * H * 4);
@@ -105,11 +106,11 @@ int forward_tile_m(const moe_config* c, int T) {
 // Whether moe_forward_fused runs its single expert-half launch for T tokens:
 // at most 4096 pairs (the one-launch quantize + dispatch), entries of at most
 // 64 rows, and NVFP4 activation scales per row (a per-tensor h scale needs
-// every h row before any is quantized).
+// every h row before any is quantized); not MXFP4.
 bool fused_applies(const moe_config* c, int T) {
   const long P = (long)T * c->top_k;
   const bool nv = c->fmt == MOE_FMT_NVFP4;
-  return T > 0 && P <= kSmallDispatchPairs && forward_tile_m(c, T) <= 64 &&
+  return T > 0 && c->fmt != MOE_FMT_MXFP4 && P <= kSmallDispatchPairs && forward_tile_m(c, T) <= 64 &&
          (!nv || c->act_gs == MOE_ACT_GS_PER_ROW);
 }
 
@@ -168,10 +169,23 @@ uint64_t next_epoch() {
 
 // Whether moe_route_forward runs routing, x quantization and dispatch as
 // one launch: small batches (T <= 256, T k <= 4096) without a per-tensor
-// NVFP4 x scale (which needs its maximum before any row).
+// NVFP4 x scale (which needs its maximum before any row); not MXFP4.
 bool route_forward_one_launch(const moe_config* c, int T) {
-  return T > 0 && T <= kRoutePrepMaxTokens && (long)T * c->top_k <= kSmallDispatchPairs &&
+  return T > 0 && c->fmt != MOE_FMT_MXFP4 && T <= kRoutePrepMaxTokens && (long)T * c->top_k <= kSmallDispatchPairs &&
          !(c->fmt == MOE_FMT_NVFP4 && c->act_gs == MOE_ACT_GS_PER_TENSOR);
+}
+
+// Whether fmt is one the encoders and the layer take.
+bool known_fmt(int fmt) { return fmt == MOE_FMT_NVFP4 || fmt == MOE_FMT_MXFP8 || fmt == MOE_FMT_MXFP4; }
+
+// The balance loss takes its experts, slots and gate form from the
+// configuration; the rest of it is the expert half's.
+int check_balance(const moe_config* c, int T, int S) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->num_experts < 1 || c->num_experts > 1024) return MOE_ERR_INVALID_ARG;
+  if (c->top_k < 1 || c->top_k > 32 || c->top_k > c->num_experts) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || T > (1 << 26) || S < 1 || S > 65535) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
 }
 
 bool test_fail_requested() {
@@ -207,7 +221,7 @@ int moe_check_arch(const char* arch) {
 
 int moe_validate_config(const moe_config* c) {
   if (c == nullptr) return MOE_ERR_INVALID_ARG;
-  if (c->fmt != MOE_FMT_NVFP4 && c->fmt != MOE_FMT_MXFP8) return MOE_ERR_UNSUPPORTED_FORMAT;
+  if (!known_fmt(c->fmt)) return MOE_ERR_UNSUPPORTED_FORMAT;
   if (c->hidden <= 0 || c->hidden % 128 != 0 || c->hidden > (1 << 16)) return MOE_ERR_INVALID_ARG;
   if (c->ffn <= 0 || c->ffn % 128 != 0 || c->ffn > (1 << 16)) return MOE_ERR_INVALID_ARG;
   if (c->num_experts < 1 || c->num_experts > 1024) return MOE_ERR_INVALID_ARG;
@@ -279,7 +293,7 @@ int moe_cap_swiglu(const moe_config* c, const float* g, const float* u, int64_t 
 int moe_encode_weights(int32_t fmt, int32_t dtype, const void* w, int32_t nmat, int32_t rows, int32_t cols,
                        uint8_t* codes, uint8_t* scales, float* gs, int32_t gs_group, int32_t gs_stride,
                        void* ws, size_t ws_bytes, void* stream) {
-  if (fmt != MOE_FMT_NVFP4 && fmt != MOE_FMT_MXFP8) return MOE_ERR_UNSUPPORTED_FORMAT;
+  if (!known_fmt(fmt)) return MOE_ERR_UNSUPPORTED_FORMAT;
   if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
   if (nmat < 0 || rows <= 0 || cols <= 0 || cols % 32 != 0) return MOE_ERR_INVALID_ARG;
   if ((long)nmat * rows > (1L << 30) || (long)nmat * rows * cols > (1L << 40)) return MOE_ERR_INVALID_ARG;
@@ -302,7 +316,7 @@ int moe_encode_weights(int32_t fmt, int32_t dtype, const void* w, int32_t nmat, 
 int moe_decode_weights(int32_t fmt, const uint8_t* codes, const uint8_t* scales, const float* gs,
                        int32_t gs_group, int32_t gs_stride, int32_t nmat, int32_t rows, int32_t cols, float* out,
                        void* stream) {
-  if (fmt != MOE_FMT_NVFP4 && fmt != MOE_FMT_MXFP8) return MOE_ERR_UNSUPPORTED_FORMAT;
+  if (!known_fmt(fmt)) return MOE_ERR_UNSUPPORTED_FORMAT;
   if (nmat < 0 || rows <= 0 || cols <= 0 || cols % 32 != 0) return MOE_ERR_INVALID_ARG;
   if ((long)nmat * rows > (1L << 30) || (long)nmat * rows * cols > (1L << 40)) return MOE_ERR_INVALID_ARG;
   if (nmat == 0) return MOE_OK;
@@ -338,6 +352,134 @@ int moe_route(const moe_config* c, const void* x, int32_t T, const void* w_route
              : MOE_ERR_LAUNCH;
 }
 
+int moe_route_logits(const moe_config* c, int32_t T, const void* ws, size_t ws_bytes, float* z, void* stream) {
+  int st = moe_validate_config(c);
+  if (st != MOE_OK) return st;
+  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(c, T, const_cast<void*>(ws), ws_bytes)) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (z == nullptr || !aligned(z, 4)) return MOE_ERR_INVALID_ARG;
+  if ((st = device_check()) != MOE_OK) return st;
+  const Layout L = layout(c, c->max_tokens);
+  return launch_router_logits_sum(at<float>(const_cast<void*>(ws), L.z), T, c->num_experts, z,
+                                  static_cast<hipStream_t>(stream)) == 0
+             ? MOE_OK
+             : MOE_ERR_LAUNCH;
+}
+
+int moe_balance_workspace_size(const moe_config* c, int32_t T, int32_t S, size_t* bytes) {
+  const int st = check_balance(c, T, S);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = balance_ws_bytes(T, c->num_experts, S);
+  return MOE_OK;
+}
+
+int moe_balance_forward(const moe_config* c, int32_t dtype, const void* z, int32_t T, const int32_t* topk_ids,
+                        const int32_t* seq_offsets, int32_t S, const uint8_t* token_mask, int32_t* counts,
+                        int32_t* live, float* probs, float* loss, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_balance(c, T, S);
+  if (st != MOE_OK) return st;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (S > 1 && seq_offsets == nullptr) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (z == nullptr || topk_ids == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (counts == nullptr || live == nullptr || probs == nullptr || loss == nullptr || ws == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(z, dtype == MOE_DTYPE_BF16 ? 2 : 4) || !aligned(topk_ids, 4) || !aligned(seq_offsets, 4) ||
+      !aligned(counts, 4) || !aligned(live, 4) || !aligned(probs, 4) || !aligned(loss, 4) || !aligned(ws, 256))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < balance_ws_bytes(T, c->num_experts, S)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if ((st = device_check()) != MOE_OK) return st;
+  BalanceArgs a{};
+  a.z = z;
+  a.dtype = dtype;
+  a.T = T;
+  a.E = c->num_experts;
+  a.k = c->top_k;
+  a.ids = topk_ids;
+  a.bounds = seq_offsets;
+  a.S = S;
+  a.mask = token_mask;
+  a.counts = counts;
+  a.live = live;
+  a.probs = probs;
+  a.loss = loss;
+  a.ws = ws;
+  return launch_balance_forward(a, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_balance_backward(const moe_config* c, int32_t dtype, const void* z, int32_t T, const int32_t* topk_ids,
+                         const int32_t* seq_offsets, int32_t S, const uint8_t* token_mask, const int32_t* counts,
+                         const int32_t* live, const float* d_loss, const float* d_topk_w, void* dz, void* stream) {
+  int st = check_balance(c, T, S);
+  if (st != MOE_OK) return st;
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (S > 1 && seq_offsets == nullptr) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (z == nullptr || counts == nullptr || live == nullptr || d_loss == nullptr || dz == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (d_topk_w != nullptr && topk_ids == nullptr) return MOE_ERR_INVALID_ARG;
+  const uintptr_t el = dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  if (!aligned(z, el) || !aligned(dz, el) || !aligned(topk_ids, 4) || !aligned(seq_offsets, 4) ||
+      !aligned(counts, 4) || !aligned(live, 4) || !aligned(d_loss, 4) || !aligned(d_topk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = device_check()) != MOE_OK) return st;
+  BalanceArgs a{};
+  a.z = z;
+  a.dtype = dtype;
+  a.T = T;
+  a.E = c->num_experts;
+  a.k = c->top_k;
+  a.ids = topk_ids;
+  a.bounds = seq_offsets;
+  a.S = S;
+  a.mask = token_mask;
+  a.counts = const_cast<int32_t*>(counts);
+  a.live = const_cast<int32_t*>(live);
+  a.d_loss = d_loss;
+  a.d_w = d_topk_w;
+  a.norm_topk = c->norm_topk;
+  a.routed_scale = c->routed_scale;
+  a.dz = dz;
+  return launch_balance_backward(a, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, int32_t a_rows,
+                      const int32_t* row_ids, int32_t id_div, int32_t M, const uint8_t* w, const uint8_t* w_scales,
+                      int32_t G, int32_t N, int32_t K, const int32_t* offsets, int32_t out_dtype, void* out,
+                      void* stream) {
+  if (fmt != MOE_FMT_MXFP4) return MOE_ERR_UNSUPPORTED_FORMAT;
+  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (a_rows < 0 || M < 0 || G < 1 || G > 1024 || N < 1 || N > (1 << 20)) return MOE_ERR_INVALID_ARG;
+  if (K < 32 || K % 32 != 0 || K > (1 << 20)) return MOE_ERR_INVALID_ARG;
+  if (M > (1 << 26) || a_rows > (1 << 26) || (row_ids != nullptr && id_div < 1)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (a_rows == 0 || a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr ||
+      offsets == nullptr || out == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(a_scales, 4) || !aligned(w_scales, 4) ||
+      !aligned(row_ids, 4) || !aligned(offsets, 4))
+    return MOE_ERR_INVALID_ARG;
+  const int st = device_check();
+  if (st != MOE_OK) return st;
+  ProductArgs p{};
+  p.a = a;
+  p.a_sc = a_scales;
+  p.a_rows = a_rows;
+  p.row_ids = row_ids;
+  p.id_div = id_div;
+  p.M = M;
+  p.w = w;
+  p.w_sc = w_scales;
+  p.G = G;
+  p.N = N;
+  p.K = K;
+  p.offsets = offsets;
+  p.out = out;
+  p.out_f32 = out_dtype == MOE_DTYPE_F32;
+  return launch_group_product(p, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
 int moe_dispatch(const moe_config* c, const int32_t* topk_ids, int32_t T, int32_t* expert_offsets,
                  int32_t* sorted_pairs, int32_t* pair_pos, void* ws, size_t ws_bytes, void* stream) {
   int st = moe_validate_config(c);
@@ -367,6 +509,7 @@ int moe_prepare_weights(const moe_config* c, const moe_expert_weights* src, moe_
   int st = moe_validate_config(c);
   if (st != MOE_OK) return st;
   if (src == nullptr || dst == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->fmt == MOE_FMT_MXFP4) return MOE_ERR_UNSUPPORTED_FORMAT;   // no packed layout
   if (src->layout != MOE_LAYOUT_CANONICAL) return MOE_ERR_INVALID_ARG;
   if (src->w13 == nullptr || src->w13_sc == nullptr || src->w2 == nullptr || src->w2_sc == nullptr ||
       dst->w13 == nullptr || dst->w13_sc == nullptr || dst->w2 == nullptr || dst->w2_sc == nullptr)
@@ -402,6 +545,7 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
     return MOE_ERR_INVALID_ARG;
   if (c->fmt == MOE_FMT_NVFP4 && w->gs == nullptr) return MOE_ERR_INVALID_ARG;
   if (w->layout != MOE_LAYOUT_CANONICAL && w->layout != MOE_LAYOUT_PACKED) return MOE_ERR_INVALID_ARG;
+  if (c->fmt == MOE_FMT_MXFP4 && w->layout != MOE_LAYOUT_CANONICAL) return MOE_ERR_INVALID_ARG;
   // the kernels' 16-byte vector loads and stores
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(w->w13, 16) || !aligned(w->w2, 16) ||
       !aligned(w->w13_sc, 4) || !aligned(w->w2_sc, 4) || !aligned(w->gs, 4) || !aligned(topk_ids, 4) ||
@@ -431,7 +575,7 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
   const ActGs agx = act_gs_of(c, 0, ags), agh = act_gs_of(c, 1, ags);
   if (prep_done) {
     // x quantized and dispatched by moe_route_forward's first launch
-  } else if (P <= kSmallDispatchPairs) {
+  } else if (P <= kSmallDispatchPairs && c->fmt != MOE_FMT_MXFP4) {
     // 1 + 2. quantize x per row and dispatch (+ tile list) in one launch; the
     // quantize-x stage covers both, the dispatch stage is empty
     record(events, 2 * MOE_STAGE_QUANT_X, s);
@@ -455,6 +599,57 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
     record(events, 2 * MOE_STAGE_DISPATCH, s);
     bad |= launch_dispatch(topk_ids, P, c->expert_begin, EL, tile_m, b, s);
     record(events, 2 * MOE_STAGE_DISPATCH + 1, s);
+  }
+
+  // y larger than the last-level cache streams (non-temporal stores in the
+  // down epilogue, loads in the combine); its size is taken at the expected
+  // local pair count, the one the tile height follows
+  const size_t y_bytes = (size_t)T * k * EL / c->num_experts * H * sizeof(float);
+  const bool stream_y = y_bytes > kStreamBytes;
+
+  if (c->fmt == MOE_FMT_MXFP4) {
+    // 3-5. the gate/up product over the dispatched rows, the capped SwiGLU
+    // with h's encoding, the down product
+    ProductArgs gp{};
+    gp.a = at<uint8_t>(ws, L.xq);
+    gp.a_sc = at<uint8_t>(ws, L.xs);
+    gp.a_rows = T;
+    gp.row_ids = b.sorted;
+    gp.id_div = k;
+    gp.M = P;
+    gp.w = w->w13;
+    gp.w_sc = w->w13_sc;
+    gp.G = EL;
+    gp.N = 2 * F;
+    gp.K = H;
+    gp.offsets = b.offsets;
+    gp.out = at<float>(ws, L.h);
+    gp.out_f32 = 1;
+    ProductArgs dp = gp;
+    dp.a = at<uint8_t>(ws, L.hq);
+    dp.a_sc = at<uint8_t>(ws, L.hs);
+    dp.a_rows = P;
+    dp.row_ids = nullptr;
+    dp.w = w->w2;
+    dp.w_sc = w->w2_sc;
+    dp.N = H;
+    dp.K = F;
+    dp.out = at<float>(ws, L.y);
+    record(events, 2 * MOE_STAGE_GATE_UP, s);
+    bad |= launch_group_product(gp, s);
+    record(events, 2 * MOE_STAGE_GATE_UP + 1, s);
+    record(events, 2 * MOE_STAGE_QUANT_H, s);
+    bad |= launch_swiglu_mxfp4(at<float>(ws, L.h), P, b.offsets + EL, F, c->cap_form,
+                               c->cap_form == MOE_CAP_NONE ? 1.0f : c->cap, at<uint8_t>(ws, L.hq),
+                               at<uint8_t>(ws, L.hs), s);
+    record(events, 2 * MOE_STAGE_QUANT_H + 1, s);
+    record(events, 2 * MOE_STAGE_DOWN, s);
+    bad |= launch_group_product(dp, s);
+    record(events, 2 * MOE_STAGE_DOWN + 1, s);
+    record(events, 2 * MOE_STAGE_COMBINE, s);
+    bad |= launch_combine(at<float>(ws, L.y), b.pos, topk_w, T, k, H, stream_y, static_cast<uint16_t*>(out), s);
+    record(events, 2 * MOE_STAGE_COMBINE + 1, s);
+    return bad ? MOE_ERR_LAUNCH : MOE_OK;
   }
 
   // 3. gate/up GEMM + capped SwiGLU -> h (fp32, sorted rows)
@@ -492,11 +687,6 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
   d.w_codes = w->w2;
   d.w_sc = w->w2_sc;
   d.out = at<float>(ws, L.y);
-  // y larger than the last-level cache streams (non-temporal stores in the
-  // down epilogue, loads in the combine); its size is taken at the expected
-  // local pair count, the one the tile height follows
-  const size_t y_bytes = (size_t)T * k * EL / c->num_experts * H * sizeof(float);
-  const bool stream_y = y_bytes > kStreamBytes;
   d.stream_out = stream_y ? 1 : 0;
 
   if (fused) {

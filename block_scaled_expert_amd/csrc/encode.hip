@@ -1,6 +1,6 @@
 // Expert weight encoding and decoding on the GPU: bf16 / fp32 matrices to
 // the canonical NVFP4 or MXFP8 layout with freshly computed scales, and back
-// to fp32.  Weight sync re-encodes experts this way (Miles docs
+// to fp32 (MXFP4: mxfp4.hip).  Weight sync re-encodes experts this way (Miles docs
 // "inkling-2-small", section 5 on weight updates; the fp32 scale of NVFP4 is
 // recomputed from the data on every encode), and the format definitions are
 // those of the checkpoint (SGLang cookbook "Inkling-2-Small", section 2
@@ -131,8 +131,8 @@ int launch_encode_weights(int fmt, int dtype, const void* w, int nmat, int rows,
                           uint8_t* scales, float* gs, int gs_group, int gs_stride, uint32_t* amax,
                           hipStream_t stream) {
   if (nmat <= 0 || rows <= 0) return 0;
-  if (fmt == 2)
-    return launch_quant(2, dtype, w, nmat * rows, nullptr, cols, codes, scales, nullptr, stream);
+  if (fmt != 1)
+    return launch_quant(fmt, dtype, w, nmat * rows, nullptr, cols, codes, scales, nullptr, stream);
   const long per_mat = (long)rows * cols;
   hipLaunchKernelGGL(k_zero_u32, dim3(ceil_div(nmat, 256)), dim3(256), 0, stream, amax, nmat);
   const int chunks = (int)std::min<long>(ceil_div(per_mat, 256L * 16), 64L);
@@ -158,6 +158,7 @@ int launch_decode_weights(int fmt, const uint8_t* codes, const uint8_t* scales, 
                           int cols, int gs_group, int gs_stride, float* out, hipStream_t stream) {
   if (nmat <= 0 || rows <= 0) return 0;
   const long per_mat = (long)rows * cols;
+  if (fmt == 4) return launch_mxfp4_decode(codes, scales, (long)nmat * per_mat, out, stream);
   const long nblocks = (long)nmat * per_mat / (fmt == 1 ? 16 : 32);
   const dim3 g(ceil_div(nblocks, 256L));
   if (fmt == 1)

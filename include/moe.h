@@ -45,6 +45,7 @@
  *    row, and one fp32 scale per scale domain (a row of activations; one per
  *    (expert, matrix) for weights).
  *  - MXFP8 = E4M3 elements, one E8M0 scale per 32 consecutive elements.
+ *  - MXFP4 = E2M1 elements, one E8M0 scale per 32 consecutive elements.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -69,7 +70,9 @@ enum moe_status {
                                       than its fixed scratch buffer */
 };
 
-enum moe_fmt { MOE_FMT_NVFP4 = 1, MOE_FMT_MXFP8 = 2 };
+/* MXFP4 runs the expert products at the matrix cores' FP4 rate (both operands
+ * go to them as stored).  The value 3 is not assigned. */
+enum moe_fmt { MOE_FMT_NVFP4 = 1, MOE_FMT_MXFP8 = 2, MOE_FMT_MXFP4 = 4 };
 
 /* Cap applied around the SwiGLU; c = cfg->cap.
  * SOFT_GATE_UP: g' = c tanh(g/c), u' = c tanh(u/c), h = silu(g') u'
@@ -97,7 +100,7 @@ enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
  *  PER_TENSOR: one for the whole tensor of the call, max / 2688 over all T
  *              x rows, and over all local (token, expert) h rows.
  *  STATIC:     the fixed values act_gs_static[0] (x) and [1] (h).
- * MXFP8 carries no fp32 scale and ignores this field. */
+ * MXFP8 and MXFP4 carry no fp32 scale and ignore this field. */
 enum moe_act_gs { MOE_ACT_GS_PER_ROW = 0, MOE_ACT_GS_PER_TENSOR = 1, MOE_ACT_GS_STATIC = 2 };
 
 /* Layer configuration (host struct, read during the call only). */
@@ -138,6 +141,9 @@ enum moe_layout {
  *  MXFP8: w13    [i][2F][H]     E4M3 codes; w13_sc [i][2F][H/32] E8M0
  *         w2     [i][H][F]      E4M3 codes; w2_sc  [i][H][F/32]  E8M0
  *         gs     unused (may be NULL).
+ *  MXFP4: w13    [i][2F][H/2]   E2M1 codes; w13_sc [i][2F][H/32] E8M0
+ *         w2     [i][H][F/2]    E2M1 codes; w2_sc  [i][H][F/32]  E8M0
+ *         gs     unused (may be NULL).  Canonical layout only.
  * The packed layout holds exactly the same arrays (same sizes, same gs) with
  * the bytes of every 16-row x 128-column tile reordered so that each
  * wavefront load of the expert GEMMs reads one contiguous kilobyte. */
@@ -201,6 +207,10 @@ int moe_workspace_size(const moe_config* cfg, size_t* bytes);
  *  MXFP8: codes [rows][cols], scales [rows][cols/32] E8M0, row_gs unused.
  *         Per block of 32: X = 2^(floor(log2 amax) - 8) (2^-127 for a zero
  *         block), codes E4M3(v / X) saturating.
+ *  MXFP4: codes [rows][cols/2], scales [rows][cols/32] E8M0, row_gs unused.
+ *         Per block of 32: X = 2^(floor(log2 amax) - 2), the exponent at
+ *         least -127 (2^-127 for a zero block), codes E2M1(v / X), to nearest
+ *         even, saturating at 6; a NaN element encodes as +0.
  * ws: device scratch of at least 1028 bytes, 4-byte aligned, for NVFP4 with
  * PER_TENSOR (two passes: partial maxima, then the shared scale); unused
  * (may be NULL) otherwise.  The result is bit-identical to the definition
@@ -235,6 +245,8 @@ int moe_cap_swiglu(const moe_config* cfg, const float* g, const float* u, int64_
  *     ws: device scratch of at least 4 * nmat bytes (caller-owned).
  *  MXFP8: codes [nmat][rows][cols], E8M0 scales [nmat][rows][cols/32]
  *     exactly as moe_quantize_act; gs, gs_group, gs_stride and ws unused.
+ *  MXFP4: codes [nmat][rows][cols/2], E8M0 scales [nmat][rows][cols/32]
+ *     exactly as moe_quantize_act; gs, gs_group, gs_stride and ws unused.
  * Asynchronous on `stream`; bit-identical to the definition.  Errors:
  * MOE_ERR_UNSUPPORTED_FORMAT, MOE_ERR_INVALID_ARG (shape, alignment, null
  * pointers), MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_UNSUPPORTED_DEVICE,
@@ -246,8 +258,9 @@ int moe_encode_weights(int32_t fmt, int32_t dtype, const void* w, int32_t nmat, 
 /* moe_decode_weights: the inverse view, to fp32 [nmat][rows][cols]: NVFP4
  * element = (E2M1 value * E4M3 block scale) * gs (the first product exact,
  * one fp32 rounding), MXFP8 element = E4M3 value * 2^(scale - 127) (one
- * fp32 rounding; may overflow to inf above the fp32 range).  Layouts and gs
- * addressing as in moe_encode_weights; codes 8-byte aligned. */
+ * fp32 rounding; may overflow to inf above the fp32 range), MXFP4 element =
+ * E2M1 value * 2^(scale - 127) (likewise).  Layouts and gs addressing as in
+ * moe_encode_weights; codes 8-byte aligned, for MXFP4 out 16. */
 int moe_decode_weights(int32_t fmt, const uint8_t* codes, const uint8_t* scales, const float* gs,
                        int32_t gs_group, int32_t gs_stride, int32_t nmat, int32_t rows, int32_t cols, float* out,
                        void* stream);
@@ -265,6 +278,81 @@ int moe_decode_weights(int32_t fmt, const uint8_t* codes, const uint8_t* scales,
 int moe_route(const moe_config* cfg, const void* x, int32_t T, const void* w_router,
               const float* bias, int32_t* topk_ids, float* topk_w, uint8_t* near_tie,
               void* ws, size_t ws_bytes, void* stream);
+
+/* The fp32 logits z [T][E] that the last moe_route or moe_route_forward call
+ * on workspace ws (same cfg and T) selected from: the sigmoid of z[t][e] is
+ * the score s the call used, bit for bit.  What the router's losses and
+ * their gradients (moe_balance_forward / _backward) start from.  Before any
+ * such call the result is whatever the workspace holds. */
+int moe_route_logits(const moe_config* cfg, int32_t T, const void* ws, size_t ws_bytes, float* z, void* stream);
+
+/* Balance loss of the router, per sequence of tokens, with the per-expert
+ * counts.  For the n live tokens of a sequence, s = sigmoid(z), E =
+ * cfg->num_experts, k = cfg->top_k:
+ *   p[t][e] = s[t][e] / sum_i s[t][i]
+ *   counts[e] = number of (t, j) with topk_ids[t][j] == e
+ *   probs[e]  = mean over t of p[t][e]
+ *   loss      = E / (k n) * sum_e counts[e] probs[e]     (1 when balanced)
+ *  z [T][E] logits, bf16 or fp32 (dtype), 2- or 4-byte aligned; topk_ids
+ *  [T][k], ids outside [0, E) are not counted.  seq_offsets [S+1] ascending:
+ *  sequence s holds tokens seq_offsets[s] .. seq_offsets[s+1]-1 (any length,
+ *  also none); NULL with S = 1: one sequence of all T tokens.  Tokens
+ *  outside every sequence do not count.  token_mask [T] bytes (may be NULL):
+ *  tokens with 0 are not live; nothing of them is read.
+ *  Outputs: counts [S][E] int32, live [S] int32 (n), probs [S][E], loss [S]
+ *  fp32; a sequence without live tokens gives zeros.  Logits may be -inf (an
+ *  expert switched off; a row of only -inf has p = 0); a NaN makes its
+ *  sequence's probs and loss NaN.
+ *  ws: moe_balance_workspace_size bytes of device scratch, 256-byte aligned,
+ *  no initial contents needed.  Of cfg only num_experts (at most 1024) and
+ *  top_k (at most 32) are read.  T at most 2^26, 1 <= S <= 65535.  Two
+ *  launches; the same inputs give the same bits. */
+int moe_balance_workspace_size(const moe_config* cfg, int32_t T, int32_t S, size_t* bytes);
+int moe_balance_forward(const moe_config* cfg, int32_t dtype, const void* z, int32_t T, const int32_t* topk_ids,
+                        const int32_t* seq_offsets, int32_t S, const uint8_t* token_mask, int32_t* counts,
+                        int32_t* live, float* probs, float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/* The router's whole gradient with respect to its logits: of sum_s
+ * d_loss[s] loss[s] (the counts carry no gradient) plus, with d_topk_w not
+ * NULL, what reaches the logits through the gate weights topk_w of
+ * moe_route (cfg->norm_topk, cfg->routed_scale):
+ *   dz[t][e] = p (1 - s) (g[e] - sum_i g[i] p[t][i]),
+ *              g[e] = d_loss E counts[e] / (k n^2)
+ *   dz[t][id_j] += routed_scale v_j (1 - s_j) (d_topk_w[t][j] - sum_i d_topk_w[t][i] v_i),
+ *              v_j = s_j / sum_i s_i over the token's slots   (norm_topk), or
+ *   dz[t][id_j] += routed_scale s_j (1 - s_j) d_topk_w[t][j]
+ *  Slots with ids outside [0, E) take no part.  counts and live are
+ *  moe_balance_forward's; dz [T][E] has z's type (sums in fp32, one
+ *  rounding).  Rows of masked tokens and of tokens outside every sequence
+ *  are zero.  dz may not overlap z.  Other arguments as above; topk_ids may
+ *  be NULL when d_topk_w is.  Stateless, one launch. */
+int moe_balance_backward(const moe_config* cfg, int32_t dtype, const void* z, int32_t T, const int32_t* topk_ids,
+                         const int32_t* seq_offsets, int32_t S, const uint8_t* token_mask, const int32_t* counts,
+                         const int32_t* live, const float* d_loss, const float* d_topk_w, void* dz, void* stream);
+
+/* Grouped product of block-scaled rows and matrices, the experts' linear
+ * step on its own: for every group g and row r in [offsets[g], offsets[g+1])
+ *   out[r][n] = sum_k A[src(r)][k] W[g][n][k],
+ *   src(r) = row_ids == NULL ? r : row_ids[r] / id_div
+ * (with moe_dispatch's offsets and sorted pairs and id_div = top_k, the
+ * pairs' token rows; G = 1 is a plain matrix product).  Products of the
+ * coded values are exact, sums are fp32, out is fp32 or bf16 (out_dtype,
+ * one rounding to nearest even).
+ *  fmt: MOE_FMT_MXFP4 (others: MOE_ERR_UNSUPPORTED_FORMAT).
+ *  a [a_rows][K/2], a_scales [a_rows][K/32] as moe_quantize_act writes them;
+ *  w [G][N][K/2], w_scales [G][N][K/32] as moe_encode_weights does; a
+ *  scale byte of 255 (E8M0's NaN, never written by either) gives NaN.
+ *  offsets [G+1] ascending, within [0, M] (values outside are clamped); a
+ *  group may be empty.  out [M][N]; rows in no group are not written.  A row
+ *  whose source lies outside [0, a_rows) is zero.  out may not overlap the
+ *  inputs.
+ *  K a multiple of 32 up to 2^20, 1 <= N <= 2^20, 1 <= G <= 1024, M and
+ *  a_rows at most 2^26.  a, w and out 16-byte aligned, the other arrays 4.
+ * No workspace; one launch.  Which kernel runs follows the mean group M / G. */
+int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, int32_t a_rows,
+                      const int32_t* row_ids, int32_t id_div, int32_t M, const uint8_t* w, const uint8_t* w_scales,
+                      int32_t G, int32_t N, int32_t K, const int32_t* offsets, int32_t out_dtype, void* out,
+                      void* stream);
 
 /* Dispatch of (token, slot) pairs to the local experts: a stable counting
  * sort of the pair ids p = t*k + j by expert id (the "dispatch" stage of the
@@ -296,7 +384,9 @@ int moe_dispatch(const moe_config* cfg, const int32_t* topk_ids, int32_t T,
  *  MXFP8 codes: 2048 B per tile, lane l's bytes for columns
  *         128s + 16(l/16) + [0,16) at 16 l and for columns
  *         128s + 64 + 16(l/16) + [0,16) at 1024 + 16 l; scales: 64 B per
- *         tile, lane l's E8M0 byte (block 4s + l/16) at l. */
+ *         tile, lane l's E8M0 byte (block 4s + l/16) at l.
+ *  MXFP4 has no packed layout (MOE_ERR_UNSUPPORTED_FORMAT): its products read
+ *         the canonical arrays. */
 int moe_prepare_weights(const moe_config* cfg, const moe_expert_weights* src, moe_expert_weights* dst,
                         void* stream);
 
@@ -312,9 +402,11 @@ int moe_prepare_weights(const moe_config* cfg, const moe_expert_weights* src, mo
  *  pointing at device arrays).  events: optional stage timing (host array of
  *  2*MOE_STAGE_COUNT hipEvent_t, or NULL; events[2s] is recorded before stage
  *  s and events[2s+1] after it).  Stages that share a launch: with at most
- *  4096 (token, slot) pairs, x quantization and dispatch run as one kernel,
- *  timed by the QUANT_X pair (the DISPATCH pair is recorded back to back);
- *  in MXFP8, h is encoded by the gate/up kernel (the QUANT_H pair is empty). */
+ *  4096 (token, slot) pairs, x quantization and dispatch run as one kernel
+ *  (MXFP4 excepted), timed by the QUANT_X pair (the DISPATCH pair is recorded back to back);
+ *  in MXFP8, h is encoded by the gate/up kernel (the QUANT_H pair is empty).
+ *  MXFP4: the products are moe_group_product's (gate/up to fp32), and the
+ *  capped SwiGLU runs with h's encoding, timed by the QUANT_H pair. */
 int moe_forward(const moe_config* cfg, const void* x, int32_t T, const int32_t* topk_ids,
                 const float* topk_w, const moe_expert_weights* weights, void* out,
                 void* ws, size_t ws_bytes, void* stream, void* const* events);
@@ -337,14 +429,16 @@ int moe_forward(const moe_config* cfg, const void* x, int32_t T, const int32_t* 
  * (T * top_k / num_experts) are at most 48; other batches run moe_forward's
  * launch sequence.  events: the GATE_UP pair times the single launch;
  * the QUANT_H, DOWN and COMBINE pairs are recorded back to back after it.
- * cfg->act_gs PER_TENSOR and STATIC run the launch sequence as well. */
+ * cfg->act_gs PER_TENSOR and STATIC and the MXFP4 format run the launch
+ * sequence as well. */
 int moe_forward_fused(const moe_config* cfg, const void* x, int32_t T, const int32_t* topk_ids,
                       const float* topk_w, const moe_expert_weights* weights, void* out,
                       void* ws, size_t ws_bytes, void* stream, void* const* events);
 
 /* moe_route followed by moe_forward, with routing, x quantization and
  * dispatch in ONE launch for small batches (T <= 256 tokens and T * top_k
- * <= 4096 pairs; NVFP4 with a per-tensor activation scale excepted), where
+ * <= 4096 pairs; NVFP4 with a per-tensor activation scale and MXFP4
+ * excepted), where
  * the layer is bound by launches and the waits between them (TokenSpeed blog
  * "TML Inkling 2 Small at Day 0", the paragraph after the "What's new"
  * table; SGLang blog "SGLang and Miles Add Day-0 Support for Inkling 2

@@ -189,6 +189,39 @@ def dequantize_mxfp8(codes, scales) -> np.ndarray:
 
 
 # --------------------------------------------------------------------------
+# MXFP4: E2M1 elements, one E8M0 scale per 32 consecutive elements of a row.
+# The scale as in MXFP8 with E2M1's emax: X = 2^(floor(log2 amax) - 2),
+# exponent clamped to [-127, 127]; elements saturate to +-6.
+# --------------------------------------------------------------------------
+
+def quantize_mxfp4(v: np.ndarray):
+    """Quantize fp32 rows [..., K] (K % 32 == 0) to MXFP4.  The maximum is
+    taken over the block's numbers (a NaN encodes as +0); an infinite one
+    takes the exponent above every finite maximum's.
+
+    Returns (packed codes uint8 [..., K/2], scales uint8 [..., K/32]).
+    """
+    v = np.asarray(v, dtype=np.float32)
+    K = v.shape[-1]
+    assert K % MX_BLOCK == 0
+    blocks = v.reshape(v.shape[:-1] + (K // MX_BLOCK, MX_BLOCK)).astype(np.float64)
+    mag = np.where(np.isnan(blocks), 0.0, np.abs(blocks))
+    amax = mag.max(axis=-1)
+    _, ex = np.frexp(np.where(np.isinf(amax), 2.0 ** 128, amax))    # amax = m*2^ex
+    E = np.where(amax == 0, -127, np.clip(ex - 1 - 2, -127, 127))
+    codes = e2m1_encode((blocks * np.ldexp(1.0, -E)[..., None]).astype(np.float32))
+    return pack_nibbles(codes.reshape(-1, K)).reshape(v.shape[:-1] + (K // 2,)), (E + 127).astype(np.uint8)
+
+
+def dequantize_mxfp4(packed, scales) -> np.ndarray:
+    """MXFP4 -> float64 values (exact)."""
+    codes = unpack_nibbles(np.asarray(packed, dtype=np.uint8))
+    K = codes.shape[-1]
+    vals = e2m1_decode(codes).reshape(codes.shape[:-1] + (K // MX_BLOCK, MX_BLOCK))
+    return (vals * e8m0_decode(scales)[..., None]).reshape(codes.shape)
+
+
+# --------------------------------------------------------------------------
 # NVFP4: E2M1 elements, one E4M3 scale per 16 consecutive elements of a row,
 # one fp32 scale per scale domain (a row for activations, a whole tensor for
 # weights).

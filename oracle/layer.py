@@ -65,7 +65,7 @@ class OracleConfig:
     ffn: int
     num_experts: int
     top_k: int
-    fmt: str                      # "nvfp4" | "mxfp8"
+    fmt: str                      # "nvfp4" | "mxfp8" | "mxfp4"
     expert_begin: int = 0
     num_local: int | None = None  # None -> all experts
     cap_form: int = CAP_SOFT_GATE_UP
@@ -166,6 +166,9 @@ def quantize_rows(fmt: str, v: np.ndarray, gs=None):
     if fmt == "mxfp8":
         c, s = F.quantize_mxfp8(v)
         return dict(codes=c, scales=s)
+    if fmt == "mxfp4":
+        c, s = F.quantize_mxfp4(v)
+        return dict(codes=c, scales=s)
     if fmt == "nvfp4":
         if gs is None:
             c, s, g = F.quantize_nvfp4(v, domain="row")
@@ -194,6 +197,8 @@ def act_scale(cfg: OracleConfig, site: int, v_all: np.ndarray):
 def dequantize_rows(fmt: str, q: dict) -> np.ndarray:
     if fmt == "mxfp8":
         return F.dequantize_mxfp8(q["codes"], q["scales"])
+    if fmt == "mxfp4":
+        return F.dequantize_mxfp4(q["codes"], q["scales"])
     return F.dequantize_nvfp4(q["codes"], q["scales"], q["gs"])
 
 
@@ -204,9 +209,10 @@ def quantize_expert_weights(fmt: str, gate: np.ndarray, up: np.ndarray, down: np
     w13 rows are gate rows 0..F-1 then up rows F..2F-1 (reading R5).
     NVFP4: one fp32 scale per matrix (gate, up, down separately, R2).
     """
-    if fmt == "mxfp8":
-        c13, s13 = F.quantize_mxfp8(np.concatenate([gate, up], axis=0))
-        c2, s2 = F.quantize_mxfp8(down)
+    if fmt in ("mxfp8", "mxfp4"):
+        enc = F.quantize_mxfp8 if fmt == "mxfp8" else F.quantize_mxfp4
+        c13, s13 = enc(np.concatenate([gate, up], axis=0))
+        c2, s2 = enc(down)
         return dict(w13=c13, w13_sc=s13, w2=c2, w2_sc=s2)
     cg, sg, gg = F.quantize_nvfp4(gate, domain="tensor")
     cu, su, gu = F.quantize_nvfp4(up, domain="tensor")
@@ -217,9 +223,10 @@ def quantize_expert_weights(fmt: str, gate: np.ndarray, up: np.ndarray, down: np
 
 def dequantize_expert(fmt: str, ew: dict):
     """Expert weights -> float64 (gate [F,H], up [F,H], down [H,F])."""
-    if fmt == "mxfp8":
-        w13 = F.dequantize_mxfp8(ew["w13"], ew["w13_sc"])
-        w2 = F.dequantize_mxfp8(ew["w2"], ew["w2_sc"])
+    if fmt in ("mxfp8", "mxfp4"):
+        dec = F.dequantize_mxfp8 if fmt == "mxfp8" else F.dequantize_mxfp4
+        w13 = dec(ew["w13"], ew["w13_sc"])
+        w2 = dec(ew["w2"], ew["w2_sc"])
         Fd = w13.shape[0] // 2
         return w13[:Fd], w13[Fd:], w2
     Fd = ew["w13"].shape[0] // 2
