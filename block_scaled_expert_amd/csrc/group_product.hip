@@ -1,126 +1,207 @@
 // Grouped MXFP4 product, few rows per group (decode, ragged calls): the time
 // is that of streaming the weights of the groups that have rows.
 //
-// Work: one workgroup of 4 waves per (group, 64 weight rows).  The waves split
-// k four ways, each loads its weight pieces straight from HBM into matrix
-// operands (each weight byte is used by one wave), the partial tiles meet in
-// LDS and are added in wave order, so the result does not depend on
-// scheduling.  A group without rows costs one pair of offset reads.  A group
-// with more than 16 MS rows takes further passes over the same weights, which
-// then come from the caches.
+// Work: one workgroup of 4 waves per (group, 16 MS of its rows, run of NT tiles
+// of 64 weight rows); a wave takes 16 rows of each tile over the whole of k.  Each weight
+// byte is loaded once, by the wave that uses it, into registers (no LDS on
+// that path) through a ring of PF chunks that runs on from tile to tile.  The
+// operand wants 64 bytes of each of 16 rows; loaded that way every 128-byte
+// line is asked for twice, and the second time it is often gone.  Each load
+// takes whole lines of 8 rows instead (RawW), and two rows' halves change
+// places in registers before the product (operand_w).  The group's rows of A
+// are staged in LDS in operand order once for all tiles.  Sums over k stay in
+// one accumulator in k order, so a result depends on nothing but its own
+// operands.
 #include "group_product.h"
 
 namespace moe {
 
-constexpr int kStep = 128;   // k of one matrix instruction
+constexpr int kPanel = 18;   // chunks of A in LDS at a time (k 4608; 39 KiB per 16 rows)
 
 template <int MS>
-struct StreamLds {
-  float red[4][16 * MS][64 + 1];
-  int src[16 * MS];
+constexpr size_t stream_lds(int panel) {
+  return (size_t)MS * panel * (1024 * kU + 64 * 2) + 16 * MS * 4;
+}
+
+// One chunk of 16 weight rows as loaded: lane (r, b) = (l % 16, l / 16) holds
+// block 2 b + r / 8 of row r % 8 in q[0] and of row 8 + r % 8 in q[1]; sc is
+// row r's own.
+struct RawW {
+  v4u q[2];
+  uint16_t sc;
+  uint8_t sc1;   // odd block counts: the second scale on its own
 };
 
-template <int MS>
-__global__ __launch_bounds__(256) void k_product_stream(ProductArgs p) {
-  constexpr int TM = 16 * MS, PF = 2;
-  __shared__ StreamLds<MS> sm;
-  const int g = blockIdx.y, n0 = blockIdx.x * 64;
-  int lo, hi;
-  group_rows(p, g, lo, hi);
-  if (lo >= hi) return;
+// Lanes r and r ^ 8 exchange what the other needs (a rotation by 8 within 16
+// lanes, written to half of them): q[j] becomes block 2 b + j of row r.
+__device__ inline void operand_w(const RawW& w, Frag& f) {
+  static_assert(kU == 2, "two loads, two halves");
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int x = (int)w.q[0][i], y = (int)w.q[1][i];
+    f.q[0][i] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);   // row_ror:8 into lanes 8..15
+    f.q[1][i] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);   // into lanes 0..7
+  }
+}
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+// ODD: rows of an odd number of scale blocks, whose last chunk ends inside a
+// pair of scales (scales are then loaded one by one).
+template <int MS, int PF, bool ODD>
+__global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int panel, int NT) {
+  constexpr int TM = 16 * MS;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  v4u* const lq = reinterpret_cast<v4u*>(lds);                                     // [panel][MS][kU][64]
+  uint16_t* const ls = reinterpret_cast<uint16_t*>(lds + (size_t)panel * MS * kU * 1024);   // [panel][MS][64]
+  int* const src = reinterpret_cast<int*>(ls + (size_t)panel * MS * 64);           // [TM]
+
+  Item it;
+  if (!find_item<TM>(p, blockIdx.y, it)) return;
+  const int g = it.g, m0 = it.row0, rows = it.rows, n0 = blockIdx.x * 64 * NT;
+
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, b = lane >> 4;
-  const int nb = p.K / 32;                       // scale blocks of a row
-  const int steps = (p.K + kStep - 1) / kStep;
-  const int s0 = wave * steps / 4, s1 = (wave + 1) * steps / 4;
-  const size_t row_bytes = p.K / 2;
+  const int nb = p.K / 32;                          // scale blocks of a row
+  const int chunks = (nb + kChunkBlocks - 1) / kChunkBlocks;
+  const int tiles = min(NT, (p.N - n0 + 63) / 64);
+  const int row_bytes = p.K / 2;
+  // this wave's weight rows nw + 64 t ..; rows past N read zeros
+  const int nw = n0 + 16 * wave;
+  const int wrows = max(min(64 * NT - 16 * wave, p.N - nw), 0);
+  const size_t wr0 = (size_t)g * p.N + min(nw, p.N - 1);
+  const Buf wq = make_buf(p.w + wr0 * row_bytes, wrows * row_bytes);
+  const Buf ws = make_buf(p.w_sc + wr0 * nb, wrows * nb);
+  const int at = 2 * b + (r >> 3);                  // this lane's piece of a line
+  const uint32_t woff = (r & 7) * row_bytes + 16 * at, wsoff = r * nb + kU * b;
 
-  const uint8_t* wrow[4];
-  const uint8_t* wsc[4];
+  // chunk c of tile t
+  auto load_w = [&](int t, int c, RawW& W) {
+    const int blk = kChunkBlocks * c;
+    const bool on = t < tiles;
+    const uint32_t off = on && blk + at < nb ? woff + (uint32_t)t * (64 * row_bytes) + 16 * blk : kNowhere;
+    W.q[0] = buf16(wq, off);
+    W.q[1] = buf16(wq, off + 8 * row_bytes);
+    const uint32_t so = wsoff + (uint32_t)t * (64 * nb) + blk;
+    const bool s0 = on && blk + kU * b < nb;
+    if constexpr (ODD) {
+      W.sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)(s0 ? so : kNowhere), 0, 0);
+      W.sc1 = __builtin_amdgcn_raw_buffer_load_b8(ws, (int)(on && blk + kU * b + 1 < nb ? so + 1 : kNowhere), 0, 0);
+    } else {
+      W.sc = __builtin_amdgcn_raw_buffer_load_b16(ws, (int)(s0 ? so : kNowhere), 0, 0);
+    }
+  };
+
+  if (tid < TM) src[tid] = tid < rows ? source_row(p, m0 + tid) : -1;
+  // the first weights are on their way while the rows of A are fetched
+  RawW fw[PF];
+  int lt = 0, lc = 0;                               // the chunk that is loaded next
+  auto load_next = [&](RawW& W) {
+    load_w(lt, lc, W);
+    if (++lc == chunks) {
+      lc = 0;
+      lt++;
+    }
+  };
 #pragma unroll
-  for (int c = 0; c < 4; c++) {                  // rows past N read the last row; their columns are not stored
-    const size_t n = (size_t)g * p.N + min(n0 + 16 * c + r, p.N - 1);
-    wrow[c] = p.w + n * row_bytes;
-    wsc[c] = p.w_sc + n * nb;
+  for (int j = 0; j < PF; j++) load_next(fw[j]);
+
+  // A's chunks [p0, p0 + pn) to LDS, a 16-byte piece (one block) per thread,
+  // zeros past the end of k; rows past the tile are left as they are: a row's
+  // outputs depend on that row alone
+  auto stage_a = [&](int p0, int pn) {
+    const int pb = kChunkBlocks * pn;
+#pragma unroll 4
+    for (int i = tid; i < rows * pb; i += 256) {
+      const int row = i / pb, x = i - row * pb, blk = kChunkBlocks * p0 + x;
+      const int s = max(src[row], 0);
+      v4u v = v4u{0, 0, 0, 0};
+      uint8_t sv = 0;
+      if (blk < nb) {
+        v = *reinterpret_cast<const v4u*>(p.a + (size_t)s * row_bytes + 16 * (size_t)blk);
+        sv = p.a_sc[(size_t)s * nb + blk];
+      }
+      // block x of the panel: chunk x / 8, lane group (x % 8) / 2, instruction x % 2
+      const int c = x / kChunkBlocks, slot = c * MS + (row >> 4), l = (row & 15) + 16 * (x % kChunkBlocks / kU);
+      lq[(slot * kU + x % kU) * 64 + l] = v;
+      reinterpret_cast<uint8_t*>(ls + slot * 64 + l)[x % kU] = sv;
+    }
+  };
+  lds_barrier();                                    // src is written
+  const bool one = chunks <= panel;
+  if (one) {
+    stage_a(0, chunks);
+    lds_barrier();
   }
 
-  for (int m0 = lo; m0 < hi; m0 += TM) {
-    const int rows = min(TM, hi - m0);
-    if (tid < TM) sm.src[tid] = tid < rows ? source_row(p, m0 + tid) : -1;
-    __syncthreads();
-    const uint8_t* arow[MS];
-    const uint8_t* asc[MS];
+  v4f acc[MS];
 #pragma unroll
-    for (int i = 0; i < MS; i++) {               // rows past the tile read row 0; they are not stored
-      const size_t s = max(sm.src[16 * i + r], 0);
-      arow[i] = p.a + s * row_bytes;
-      asc[i] = p.a_sc + s * nb;
-    }
-
-    v4f acc[MS][4];
+  for (int i = 0; i < MS; i++) acc[i] = v4f{0, 0, 0, 0};
+  int t = 0, c = 0, pc = 0;                         // tile, chunk, chunk within the panel
+  while (t < tiles) {
 #pragma unroll
-    for (int i = 0; i < MS; i++)
-#pragma unroll
-      for (int c = 0; c < 4; c++) acc[i][c] = v4f{0, 0, 0, 0};
-
-    Frag fa[PF][MS], fw[PF][4];
-    auto load = [&](int step, Frag (&A)[MS], Frag (&W)[4]) {
-      const int blk = 4 * step + b, at = min(blk, nb - 1);
-#pragma unroll
-      for (int c = 0; c < 4; c++) {
-        W[c].q = *reinterpret_cast<const v4u*>(wrow[c] + 16 * (size_t)at);
-        W[c].sc = wsc[c][at];
-      }
-#pragma unroll
-      for (int i = 0; i < MS; i++) {
-        A[i].q = *reinterpret_cast<const v4u*>(arow[i] + 16 * (size_t)at);
-        A[i].sc = asc[i][at];
-        // past the last block of a row (k not a multiple of 128) A is zero
-        if (blk >= nb) A[i].q = v4u{0, 0, 0, 0};
-      }
-    };
-    if (s0 < s1) {
-#pragma unroll
-      for (int j = 0; j < PF; j++) load(min(s0 + j, s1 - 1), fa[j], fw[j]);
-    }
-    for (int s = s0; s < s1; s += PF) {
-#pragma unroll
-      for (int j = 0; j < PF; j++) {
-        if (s + j < s1) {
-#pragma unroll
-          for (int i = 0; i < MS; i++)
-#pragma unroll
-            for (int c = 0; c < 4; c++) acc[i][c] = mma4(fa[j][i], fw[j][c], acc[i][c]);
+    for (int j = 0; j < PF; j++) {
+      if (t < tiles) {
+        if (!one && pc == 0) {                      // every wave is at the same chunk
+          lds_barrier();                            // the last panel has been read
+          stage_a(c, min(panel, chunks - c));
+          lds_barrier();
         }
-        load(min(s + j + PF, s1 - 1), fa[j], fw[j]);
+        Frag A[MS], W;
+        operand_w(fw[j], W);
+        W.sc = ODD ? (uint16_t)(fw[j].sc | fw[j].sc1 << 8) : fw[j].sc;
+#pragma unroll
+        for (int i = 0; i < MS; i++) {
+#pragma unroll
+          for (int u = 0; u < kU; u++) A[i].q[u] = lq[((pc * MS + i) * kU + u) * 64 + lane];
+          A[i].sc = ls[(pc * MS + i) * 64 + lane];
+        }
+#pragma unroll
+        for (int i = 0; i < MS; i++) acc[i] = mma4<0>(A[i], W, acc[i]);
+#pragma unroll
+        for (int i = 0; i < MS; i++) acc[i] = mma4<1>(A[i], W, acc[i]);
+        pc = pc + 1 == panel ? 0 : pc + 1;
+        if (++c == chunks) {                        // the tile is done
+          const int n = nw + 64 * t + r;
+#pragma unroll
+          for (int i = 0; i < MS; i++) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+              const int m = 16 * i + 4 * b + q;
+              if (m < rows && n < p.N)
+                store_out(p, (size_t)(m0 + m) * p.N + n, src[m] < 0 ? 0.0f : acc[i][q]);
+            }
+            acc[i] = v4f{0, 0, 0, 0};
+          }
+          c = pc = 0;
+          t++;
+        }
       }
+      load_next(fw[j]);
     }
-
-#pragma unroll
-    for (int i = 0; i < MS; i++)
-#pragma unroll
-      for (int c = 0; c < 4; c++)
-#pragma unroll
-        for (int q = 0; q < 4; q++) sm.red[wave][16 * i + 4 * b + q][16 * c + r] = acc[i][c][q];
-    __syncthreads();
-    for (int idx = tid; idx < TM * 64; idx += 256) {
-      const int m = idx >> 6, c = idx & 63;
-      if (m >= rows || n0 + c >= p.N) continue;
-      float v = ((sm.red[0][m][c] + sm.red[1][m][c]) + sm.red[2][m][c]) + sm.red[3][m][c];
-      if (sm.src[m] < 0) v = 0.0f;
-      store_out(p, (size_t)(m0 + m) * p.N + n0 + c, v);
-    }
-    __syncthreads();
   }
+}
+
+// Tiles of 64 weight rows per workgroup.
+template <int MS>
+static int stream_tiles(const ProductArgs& p) {
+  const long nt = (long)ceil_div(p.N, 64) * max_items<16 * MS>(p) / 4096;
+  return (int)(nt < 1 ? 1 : nt > 4 ? 4 : nt);
+}
+
+template <int MS, int PF>
+static void launch_stream(const ProductArgs& p, hipStream_t stream) {
+  const int chunks = ceil_div(p.K, kChunkK), panel = chunks < kPanel ? chunks : kPanel, nt = stream_tiles<MS>(p);
+  const dim3 grid(ceil_div(p.N, 64 * nt), max_items<16 * MS>(p));
+  if ((p.K / 32) % 2)
+    hipLaunchKernelGGL((k_product_stream<MS, PF, true>), grid, dim3(256), stream_lds<MS>(panel), stream, p, panel, nt);
+  else
+    hipLaunchKernelGGL((k_product_stream<MS, PF, false>), grid, dim3(256), stream_lds<MS>(panel), stream, p, panel, nt);
 }
 
 int launch_group_product(const ProductArgs& p, hipStream_t stream) {
   if (p.M <= 0) return 0;
-  const dim3 grid(ceil_div(p.N, 64), p.G);
   // rows per pass from the mean group: 16 up to 16 rows, else 32
-  if ((long)p.M <= 16L * p.G) hipLaunchKernelGGL(k_product_stream<1>, grid, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL(k_product_stream<2>, grid, dim3(256), 0, stream, p);
+  if ((long)p.M <= 16L * p.G) launch_stream<1, 6>(p, stream);
+  else launch_stream<2, 4>(p, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
