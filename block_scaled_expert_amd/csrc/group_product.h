@@ -38,12 +38,19 @@ struct Frag {
 // zero and touch no memory, so ends of rows and tiles need no branches.
 typedef __amdgpu_buffer_rsrc_t Buf;
 __device__ inline Buf make_buf(const uint8_t* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)bytes, 0x00027000);
+  // the wave's lanes agree on both; saying so keeps the view in scalar registers
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<uint8_t*>((uint64_t)hi << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000);
 }
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset outside every view (views are below 2 GiB)
 
+// NT: non-temporal, for bytes that are read once.
+template <bool NT>
 __device__ inline v4u buf16(Buf b, uint32_t off) {
-  return __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, 2));
+  return __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, 0, NT ? 2 : 0));
 }
 
 template <int J>
@@ -53,17 +60,80 @@ __device__ inline v4f mma4(const Frag& a, const Frag& b, v4f c) {
   // 4, 4: both operands E2M1; J: the scale registers' byte
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, (int)a.sc, J, (int)b.sc);
 }
+// The same from codes and scales (low byte) as they are.
+__device__ inline v4f mma_codes(v4u a, int asc, v4u b, int bsc, v4f c) {
+  const v8i av = v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i bv = v8i{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, asc, 0, bsc);
+}
 
-// Work items are (group, tile of TM rows) pairs in group order.  Finds item
-// `item`: every wave of the workgroup works it out for itself, lane l counting
-// the tiles of the PER groups PER l .. (PER * 64 >= G), so that it costs one
-// round of loads and a wave scan.  Offsets are clamped to the M rows of the
-// call whatever the device array holds.  False: there are fewer items.
+// One chunk of 16 weight rows as loaded: lane (r, b) = (l % 16, l / 16) holds
+// block 2 b + r / 8 of row r % 8 in q[0] and of row 8 + r % 8 in q[1]; sc is
+// row r's own.
+struct RawW {
+  v4u q[2];
+  uint16_t sc;
+  uint8_t sc1;   // odd block counts: the second scale on its own
+};
+
+// Lanes r and r ^ 8 exchange what the other needs (a rotation by 8 within 16
+// lanes, written to half of them): q[j] becomes block 2 b + j of row r.
+template <bool ODD>
+__device__ inline void operand_w(const RawW& w, Frag& f) {
+  static_assert(kU == 2, "two loads, two halves");
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int x = (int)w.q[0][i], y = (int)w.q[1][i];
+    f.q[0][i] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);   // row_ror:8 into lanes 8..15
+    f.q[1][i] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);   // into lanes 0..7
+  }
+  f.sc = ODD ? (uint16_t)(w.sc | w.sc1 << 8) : w.sc;
+}
+
+// What a lane's loads of 16 weight rows start from: its piece of a line, its
+// byte offsets among codes and scales.
+struct WLane {
+  int at, b, nb, row8;
+  uint32_t off, soff;
+  __device__ WLane(int r, int b_, int row_bytes, int nb_)
+      : at(2 * b_ + (r >> 3)), b(b_), nb(nb_), row8(8 * row_bytes), off((r & 7) * row_bytes + 16 * (2 * b_ + (r >> 3))),
+        soff(r * nb_ + kU * b_) {}
+};
+
+// Chunk c of the 16 rows whose codes and scales start `base` and `sbase` bytes
+// into the views; nothing is loaded unless `on`.  ODD: rows of an odd number
+// of scale blocks, whose last chunk ends inside a pair of scales (they are
+// then loaded one by one).
+template <bool ODD, bool NT>
+__device__ inline void load_raw(RawW& W, Buf wq, Buf ws, const WLane& l, bool on, uint32_t base, uint32_t sbase, int c) {
+  const int blk = kChunkBlocks * c;
+  const uint32_t off = on && blk + l.at < l.nb ? l.off + base + 16 * blk : kNowhere;
+  W.q[0] = buf16<NT>(wq, off);
+  W.q[1] = buf16<NT>(wq, off + l.row8);
+  const uint32_t so = l.soff + sbase + blk;
+  const bool s0 = on && blk + kU * l.b < l.nb;
+  if constexpr (ODD) {
+    W.sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)(s0 ? so : kNowhere), 0, 0);
+    W.sc1 = __builtin_amdgcn_raw_buffer_load_b8(ws, (int)(on && blk + kU * l.b + 1 < l.nb ? so + 1 : kNowhere), 0, 0);
+  } else {
+    W.sc = __builtin_amdgcn_raw_buffer_load_b16(ws, (int)(s0 ? so : kNowhere), 0, 0);
+  }
+}
+
+// A workgroup's work: 16 MS rows (a tile) of one group and one of the nx
+// column slices.  Items are numbered tile by tile in group order, the slices
+// of a tile one after the other; the hardware hands workgroups to the 8 XCDs
+// in turn, each with its own L2, so XCD x takes the x-th eighth of the items:
+// what runs there side by side shares rows of A and the group's weights.
+// Every wave finds the item for itself, lane l counting the tiles of the PER
+// groups PER l .. (PER * 64 >= G): one round of loads and a wave scan.
+// Offsets are clamped to the M rows of the call whatever the device array
+// holds.  False: there are fewer items.
 struct Item {
-  int g, row0, rows;
+  int g, row0, rows, bx;
 };
 template <int TM, int PER>
-__device__ inline bool find_item_n(const ProductArgs& p, int item, Item& it) {
+__device__ inline bool find_item_n(const ProductArgs& p, int nx, Item& it) {
   const int lane = threadIdx.x & 63, g0 = PER * lane;
   int at[PER + 1], n = 0;
 #pragma unroll
@@ -78,10 +148,12 @@ __device__ inline bool find_item_n(const ProductArgs& p, int item, Item& it) {
     const int v = __shfl_up(end, o, kWave);
     end += lane >= o ? v : 0;
   }
-  const uint64_t past = __ballot(end > item);
-  if (past == 0) return false;
-  const int owner = __builtin_ctzll(past);
-  int left = item - (end - n), g = 0, row0 = 0, rows = 0;   // of the owner's lane
+  const int items = __builtin_amdgcn_readlane(end, 63) * nx, hw = blockIdx.x;
+  if (hw >= items) return false;
+  const int xcd = hw % 8, L = xcd * (items / 8) + min(xcd, items % 8) + hw / 8, tile = L / nx;
+  it.bx = L - tile * nx;
+  const int owner = __builtin_ctzll(__ballot(end > tile));
+  int left = tile - (end - n), g = 0, row0 = 0, rows = 0;   // meant for the owner's lane
 #pragma unroll
   for (int i = 0; i < PER; i++) {
     const int len = max(at[i + 1] - at[i], 0), tiles = (len + TM - 1) / TM;
@@ -98,17 +170,18 @@ __device__ inline bool find_item_n(const ProductArgs& p, int item, Item& it) {
   return true;
 }
 template <int TM>
-__device__ inline bool find_item(const ProductArgs& p, int item, Item& it) {
-  if (p.G <= 64) return find_item_n<TM, 1>(p, item, it);
-  if (p.G <= 512) return find_item_n<TM, 8>(p, item, it);
-  return find_item_n<TM, 16>(p, item, it);
+__device__ inline bool find_item(const ProductArgs& p, int nx, Item& it) {
+  if (p.G <= 64) return find_item_n<TM, 1>(p, nx, it);
+  if (p.G <= 512) return find_item_n<TM, 8>(p, nx, it);
+  return find_item_n<TM, 16>(p, nx, it);
 }
-// Upper bound of the items of a call.
-template <int TM>
-inline int max_items(const ProductArgs& p) {
-  const long n = p.G + (long)p.M / TM;
+// Upper bound of the tiles of a call.
+inline int max_tiles(const ProductArgs& p, int tm) {
+  const long n = p.G + (long)p.M / tm;
   return (int)(n < p.M ? n : p.M);
 }
+
+int launch_product_tile(const ProductArgs& p, hipStream_t stream);   // many rows per group
 
 // Source row of row r, -1 for a row id outside A (its output is zero).
 __device__ inline int source_row(const ProductArgs& p, int r) {
@@ -121,6 +194,13 @@ __device__ inline int source_row(const ProductArgs& p, int r) {
 __device__ inline void store_out(const ProductArgs& p, size_t i, float v) {
   if (p.out_f32) static_cast<float*>(p.out)[i] = v;
   else static_cast<__bf16*>(p.out)[i] = (__bf16)v;   // to nearest even; inf and NaN kept
+}
+
+// Four consecutive columns, i a multiple of 4.
+__device__ inline void store_out4(const ProductArgs& p, size_t i, v4f v) {
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+  if (p.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + i) = v;
+  else *reinterpret_cast<v4bf*>(static_cast<__bf16*>(p.out) + i) = __builtin_convertvector(v, v4bf);
 }
 
 }  // namespace moe

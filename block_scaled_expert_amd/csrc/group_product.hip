@@ -23,29 +23,6 @@ constexpr size_t stream_lds(int panel) {
   return (size_t)MS * panel * (1024 * kU + 64 * 2) + 16 * MS * 4;
 }
 
-// One chunk of 16 weight rows as loaded: lane (r, b) = (l % 16, l / 16) holds
-// block 2 b + r / 8 of row r % 8 in q[0] and of row 8 + r % 8 in q[1]; sc is
-// row r's own.
-struct RawW {
-  v4u q[2];
-  uint16_t sc;
-  uint8_t sc1;   // odd block counts: the second scale on its own
-};
-
-// Lanes r and r ^ 8 exchange what the other needs (a rotation by 8 within 16
-// lanes, written to half of them): q[j] becomes block 2 b + j of row r.
-__device__ inline void operand_w(const RawW& w, Frag& f) {
-  static_assert(kU == 2, "two loads, two halves");
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int x = (int)w.q[0][i], y = (int)w.q[1][i];
-    f.q[0][i] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);   // row_ror:8 into lanes 8..15
-    f.q[1][i] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);   // into lanes 0..7
-  }
-}
-
-// ODD: rows of an odd number of scale blocks, whose last chunk ends inside a
-// pair of scales (scales are then loaded one by one).
 template <int MS, int PF, bool ODD>
 __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int panel, int NT) {
   constexpr int TM = 16 * MS;
@@ -55,8 +32,8 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
   int* const src = reinterpret_cast<int*>(ls + (size_t)panel * MS * 64);           // [TM]
 
   Item it;
-  if (!find_item<TM>(p, blockIdx.y, it)) return;
-  const int g = it.g, m0 = it.row0, rows = it.rows, n0 = blockIdx.x * 64 * NT;
+  if (!find_item<TM>(p, (p.N + 64 * NT - 1) / (64 * NT), it)) return;
+  const int g = it.g, m0 = it.row0, rows = it.rows, n0 = it.bx * 64 * NT;
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, b = lane >> 4;
@@ -70,24 +47,11 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
   const size_t wr0 = (size_t)g * p.N + min(nw, p.N - 1);
   const Buf wq = make_buf(p.w + wr0 * row_bytes, wrows * row_bytes);
   const Buf ws = make_buf(p.w_sc + wr0 * nb, wrows * nb);
-  const int at = 2 * b + (r >> 3);                  // this lane's piece of a line
-  const uint32_t woff = (r & 7) * row_bytes + 16 * at, wsoff = r * nb + kU * b;
+  const WLane wl(r, b, row_bytes, nb);
 
   // chunk c of tile t
   auto load_w = [&](int t, int c, RawW& W) {
-    const int blk = kChunkBlocks * c;
-    const bool on = t < tiles;
-    const uint32_t off = on && blk + at < nb ? woff + (uint32_t)t * (64 * row_bytes) + 16 * blk : kNowhere;
-    W.q[0] = buf16(wq, off);
-    W.q[1] = buf16(wq, off + 8 * row_bytes);
-    const uint32_t so = wsoff + (uint32_t)t * (64 * nb) + blk;
-    const bool s0 = on && blk + kU * b < nb;
-    if constexpr (ODD) {
-      W.sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)(s0 ? so : kNowhere), 0, 0);
-      W.sc1 = __builtin_amdgcn_raw_buffer_load_b8(ws, (int)(on && blk + kU * b + 1 < nb ? so + 1 : kNowhere), 0, 0);
-    } else {
-      W.sc = __builtin_amdgcn_raw_buffer_load_b16(ws, (int)(s0 ? so : kNowhere), 0, 0);
-    }
+    load_raw<ODD, true>(W, wq, ws, wl, t < tiles, (uint32_t)t * (64 * row_bytes), (uint32_t)t * (64 * nb), c);
   };
 
   if (tid < TM) src[tid] = tid < rows ? source_row(p, m0 + tid) : -1;
@@ -146,8 +110,7 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
           lds_barrier();
         }
         Frag A[MS], W;
-        operand_w(fw[j], W);
-        W.sc = ODD ? (uint16_t)(fw[j].sc | fw[j].sc1 << 8) : fw[j].sc;
+        operand_w<ODD>(fw[j], W);
 #pragma unroll
         for (int i = 0; i < MS; i++) {
 #pragma unroll
@@ -181,16 +144,16 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
 }
 
 // Tiles of 64 weight rows per workgroup.
-template <int MS>
-static int stream_tiles(const ProductArgs& p) {
-  const long nt = (long)ceil_div(p.N, 64) * max_items<16 * MS>(p) / 4096;
+static int stream_tiles(const ProductArgs& p, int tm) {
+  const long nt = (long)ceil_div(p.N, 64) * max_tiles(p, tm) / 4096;
   return (int)(nt < 1 ? 1 : nt > 4 ? 4 : nt);
 }
 
 template <int MS, int PF>
 static void launch_stream(const ProductArgs& p, hipStream_t stream) {
-  const int chunks = ceil_div(p.K, kChunkK), panel = chunks < kPanel ? chunks : kPanel, nt = stream_tiles<MS>(p);
-  const dim3 grid(ceil_div(p.N, 64 * nt), max_items<16 * MS>(p));
+  const int chunks = ceil_div(p.K, kChunkK), panel = chunks < kPanel ? chunks : kPanel;
+  const int tiles = max_tiles(p, 16 * MS), nt = stream_tiles(p, 16 * MS);
+  const dim3 grid((unsigned)tiles * ceil_div(p.N, 64 * nt));
   if ((p.K / 32) % 2)
     hipLaunchKernelGGL((k_product_stream<MS, PF, true>), grid, dim3(256), stream_lds<MS>(panel), stream, p, panel, nt);
   else
@@ -199,7 +162,8 @@ static void launch_stream(const ProductArgs& p, hipStream_t stream) {
 
 int launch_group_product(const ProductArgs& p, hipStream_t stream) {
   if (p.M <= 0) return 0;
-  // rows per pass from the mean group: 16 up to 16 rows, else 32
+  // rows per workgroup from the mean group: 16, 32, and above 48 the tiled kernel
+  if ((long)p.M > 48L * p.G) return launch_product_tile(p, stream);
   if ((long)p.M <= 16L * p.G) launch_stream<1, 6>(p, stream);
   else launch_stream<2, 4>(p, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;

@@ -60,6 +60,8 @@ CASES = [
     # rows per group on both sides of every rule on the mean group
     (2, 32, 80, 256, "even"), (2, 34, 80, 256, "even"), (2, 96, 80, 256, "even"), (2, 98, 80, 256, "even"),
     (2, 128, 272, 256, "even"), (2, 130, 272, 288, "even"), (2, 514, 272, 384, "even"),
+    # enough tiles for the largest tile
+    (1, 12400, 1003, 96, "even"), (40, 2600, 1300, 672, "uneven"), (3, 8300, 1280, 160, "one"),
 ]
 
 
