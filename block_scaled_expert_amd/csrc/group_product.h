@@ -60,11 +60,12 @@ __device__ inline v4f mma4(const Frag& a, const Frag& b, v4f c) {
   // 4, 4: both operands E2M1; J: the scale registers' byte
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, (int)a.sc, J, (int)b.sc);
 }
-// The same from codes and scales (low byte) as they are.
+// The same from codes and scale words as they are.
+template <int J>
 __device__ inline v4f mma_codes(v4u a, int asc, v4u b, int bsc, v4f c) {
   const v8i av = v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const v8i bv = v8i{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, asc, 0, bsc);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, asc, J, bsc);
 }
 
 // One chunk of 16 weight rows as loaded: lane (r, b) = (l % 16, l / 16) holds
