@@ -121,11 +121,12 @@ __device__ inline void load_raw(RawW& W, Buf wq, Buf ws, const WLane& l, bool on
   }
 }
 
-// A workgroup's work: 16 MS rows (a tile) of one group and one of the nx
-// column slices.  Items are numbered tile by tile in group order, the slices
-// of a tile one after the other; the hardware hands workgroups to the 8 XCDs
-// in turn, each with its own L2, so XCD x takes the x-th eighth of the items:
-// what runs there side by side shares rows of A and the group's weights.
+// A workgroup's work: TM rows (a tile) of one group and one of the nx column
+// slices.  The hardware hands workgroups to the 8 XCDs in turn, each with its
+// own L2, so XCD x takes the x-th eighth of the items.  They are numbered
+// group by group; in a group, up to kPanelTiles tiles of one slice follow each
+// other, then come the next slices: what runs on an XCD side by side shares
+// weight slices, and a panel's rows of A stay in its L2 for all slices.
 // Every wave finds the item for itself, lane l counting the tiles of the PER
 // groups PER l .. (PER * 64 >= G): one round of loads and a wave scan.
 // Offsets are clamped to the M rows of the call whatever the device array
@@ -133,14 +134,15 @@ __device__ inline void load_raw(RawW& W, Buf wq, Buf ws, const WLane& l, bool on
 struct Item {
   int g, row0, rows, bx;
 };
-template <int TM, int PER>
-__device__ inline bool find_item_n(const ProductArgs& p, int nx, Item& it) {
+constexpr int kPanelTiles = 8;
+// `offset(i)`: the i-th of G + 1 offsets, clamped to [0, M]; hw: the
+// workgroup's number, or where one works through several, its next one.
+template <int TM, int PER, typename F>
+__device__ inline bool find_item_n(F offset, int G, int nx, int hw, Item& it) {
   const int lane = threadIdx.x & 63, g0 = PER * lane;
   int at[PER + 1], n = 0;
 #pragma unroll
-  for (int i = 0; i <= PER; i++) at[i] = p.offsets[min(g0 + i, p.G)];
-#pragma unroll
-  for (int i = 0; i <= PER; i++) at[i] = min(max(at[i], 0), p.M);
+  for (int i = 0; i <= PER; i++) at[i] = offset(min(g0 + i, G));
 #pragma unroll
   for (int i = 0; i < PER; i++) n += (max(at[i + 1] - at[i], 0) + TM - 1) / TM;
   int end = n;                                  // inclusive scan over the lanes
@@ -149,40 +151,49 @@ __device__ inline bool find_item_n(const ProductArgs& p, int nx, Item& it) {
     const int v = __shfl_up(end, o, kWave);
     end += lane >= o ? v : 0;
   }
-  const int items = __builtin_amdgcn_readlane(end, 63) * nx, hw = blockIdx.x;
+  const int items = __builtin_amdgcn_readlane(end, 63) * nx;
   if (hw >= items) return false;
-  const int xcd = hw % 8, L = xcd * (items / 8) + min(xcd, items % 8) + hw / 8, tile = L / nx;
-  it.bx = L - tile * nx;
-  const int owner = __builtin_ctzll(__ballot(end > tile));
-  int left = tile - (end - n), g = 0, row0 = 0, rows = 0;   // meant for the owner's lane
+  const int xcd = hw % 8, L = xcd * (items / 8) + min(xcd, items % 8) + hw / 8;
+  const int owner = __builtin_ctzll(__ballot(end > L / nx));
+  int left = L - (end - n) * nx, g = 0, at0 = 0, len = 0, in = 0;   // meant for the owner's lane
 #pragma unroll
   for (int i = 0; i < PER; i++) {
-    const int len = max(at[i + 1] - at[i], 0), tiles = (len + TM - 1) / TM;
-    if (left >= 0 && left < tiles) {
+    const int l = max(at[i + 1] - at[i], 0), size = (l + TM - 1) / TM * nx;
+    if (left >= 0 && left < size) {
       g = g0 + i;
-      row0 = at[i] + left * TM;
-      rows = min(TM, len - left * TM);
+      at0 = at[i];
+      len = l;
+      in = left;
     }
-    left -= tiles;
+    left -= size;
   }
   it.g = __builtin_amdgcn_readlane(g, owner);
-  it.row0 = __builtin_amdgcn_readlane(row0, owner);
-  it.rows = __builtin_amdgcn_readlane(rows, owner);
+  at0 = __builtin_amdgcn_readlane(at0, owner);
+  len = __builtin_amdgcn_readlane(len, owner);
+  in = __builtin_amdgcn_readlane(in, owner);
+  const int tiles = (len + TM - 1) / TM, panel = in / (kPanelTiles * nx), rest = in - panel * (kPanelTiles * nx);
+  const int width = min(kPanelTiles, tiles - kPanelTiles * panel);
+  it.bx = rest / width;
+  const int tile = kPanelTiles * panel + rest - it.bx * width;
+  it.row0 = at0 + tile * TM;
+  it.rows = min(TM, len - tile * TM);
   return true;
 }
-template <int TM>
-__device__ inline bool find_item(const ProductArgs& p, int nx, Item& it) {
-  if (p.G <= 64) return find_item_n<TM, 1>(p, nx, it);
-  if (p.G <= 512) return find_item_n<TM, 8>(p, nx, it);
-  return find_item_n<TM, 16>(p, nx, it);
+template <int TM, typename F>
+__device__ inline bool find_item(F offset, int G, int nx, int hw, Item& it) {
+  if (G <= 64) return find_item_n<TM, 1>(offset, G, nx, hw, it);
+  if (G <= 512) return find_item_n<TM, 8>(offset, G, nx, hw, it);
+  return find_item_n<TM, 16>(offset, G, nx, hw, it);
 }
+__device__ inline int clamped_offset(const ProductArgs& p, int i) { return min(max(p.offsets[i], 0), p.M); }
 // Upper bound of the tiles of a call.
 inline int max_tiles(const ProductArgs& p, int tm) {
   const long n = p.G + (long)p.M / tm;
   return (int)(n < p.M ? n : p.M);
 }
 
-int launch_product_tile(const ProductArgs& p, hipStream_t stream);   // many rows per group
+// Many rows per group (group_product_tile.hip).
+int launch_product_tile(const ProductArgs& p, hipStream_t stream);
 
 // Source row of row r, -1 for a row id outside A (its output is zero).
 __device__ inline int source_row(const ProductArgs& p, int r) {

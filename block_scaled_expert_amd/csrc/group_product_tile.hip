@@ -2,22 +2,24 @@
 // plain matrix products): the time is the matrix cores', if they can be fed.
 //
 // Work: one workgroup of MW x NW waves per (group, BM of its rows, BN weight
-// rows); a wave owns 16 SM rows x 16 SN weight rows.  Both operands go through
-// LDS.  The operand layout wants 16 bytes of each of 16 rows per instruction,
+// rows); a wave owns 32 SM rows x 32 SN weight rows on
+// v_mfma_scale_f32_32x32x64_f8f6f4 (measured from registers: 9.4 PFLOP/s; the
+// 16x16x128 form of the same product 4.1 to 5.4).  Both operands go through
+// LDS.  The operand layout wants 16 bytes of each of 32 rows per instruction,
 // and a load in that pattern costs the vector cache one access per lane: 17
-// bytes per clock and CU measured, against 62 where each 4 lanes share a
+// bytes per clock and CU measured, against 47 to 62 where each 4 lanes share a
 // 64-byte piece.  So the loads take a half step (k 128, 64 bytes) of 16 rows per
-// wave, row after row, and the rearrangement is left to LDS, whose 16-byte
-// columns are permuted by row so that both sides are free of bank conflicts.
+// wave, row after row, and LDS does the rearrangement.
 //
 // Pipeline, in half steps h: loads of h + 4 go to registers (ring of 2), h + 2
-// goes from there to LDS (4 slots), h is multiplied; one barrier every two.
-// Scales: 16 bytes (4 half steps) of a row per load, double-buffered, turned
-// so that a lane's 4 bytes are one word whose byte the instruction selects.
+// goes from there to LDS (3 slots), h is multiplied; one barrier a half step.
+// Scales: 16 bytes (4 half steps, a pass) of a row per load, turned so that a lane's 8 bytes are two words whose bytes the instructions
+// select.  Two workgroups share a CU (128 registers, 80 KiB of LDS each), so one
+// multiplies while the other starts, ends or waits.
 //
-// The weights are the instruction's first operand and the rows of A its
-// second, so a lane's 4 accumulator registers are 4 consecutive columns of one
-// row of out, stored together.
+// The rows of A are the instruction's first operand and the weights its second,
+// so 32 lanes of a store hold consecutive columns of one row of out: 2 cache
+// accesses an instruction, where 4 columns a lane (the other order) took 64.
 #include "group_product.h"
 
 #include <type_traits>
@@ -28,33 +30,82 @@ namespace {
 
 constexpr int kHalf = 4;                 // blocks of a half step
 
-// 16-byte column of LDS that holds block b of row `row` (rows of 64 bytes): 16
-// rows of one block fall on 16 different columns of the 256-byte bank line.
+// 16-byte column of LDS that holds block b of row `row` (rows of 64 bytes): the
+// operand's 32 rows read at 110 bytes per clock this way, at 67 in plain order.
 __device__ inline int column(int row, int b) { return b ^ ((row >> 2) & 3); }
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
+// 32 x 32 x 64: lane l holds row l % 32 and block l / 32 of the two; J: the scale words' byte.
+// Register q of lane l is out[8 (q / 4) + 4 (l / 32) + q % 4][l % 32].
+template <int J>
+__device__ inline v16f mma32(v4u a, uint32_t asc, v4u b, uint32_t bsc, v16f c) {
+  const v8i av = v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const v8i bv = v8i{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, J, (int)asc, J, (int)bsc);
+}
 
 template <int MW, int NW, int SM, int SN>
 struct Tile {
   static constexpr int sm = SM, sn = SN, nw = NW;
-  static constexpr int BM = 16 * SM * MW, BN = 16 * SN * NW, T = 64 * MW * NW;
+  static constexpr int BM = 32 * SM * MW, BN = 32 * SN * NW, T = 64 * MW * NW;
   static constexpr int PA = BM * 4 / T, PW = BN * 4 / T;   // 16-byte pieces a thread loads per half step
   static constexpr int kSlot = (BM + BN) * 64, kScale = (BM + BN) * 16;
-  static constexpr int kLds = 4 * kSlot + 2 * kScale;
-  static_assert(PA * T == BM * 4 && PW * T == BN * 4 && T >= BM + BN, "every thread has whole pieces");
+  static constexpr int kLds = 3 * kSlot + kScale;
+  static constexpr int R = (BM + BN + T - 1) / T;                            // scale rows it loads per pass
+  static_assert(PA * T == BM * 4 && PW * T == BN * 4 && T >= BM, "every thread has whole pieces");
 };
 
 }  // namespace
 
-// 4 x 4 bytes transposed: word b of the result holds byte b of every word.
-__device__ inline v4u transpose_bytes(v4u v) {
-  const uint32_t t0 = __builtin_amdgcn_perm(v[1], v[0], 0x05010400), t1 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602);
-  const uint32_t u0 = __builtin_amdgcn_perm(v[3], v[2], 0x05010400), u1 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
-  return v4u{__builtin_amdgcn_perm(u0, t0, 0x05040100), __builtin_amdgcn_perm(u0, t0, 0x07060302),
-             __builtin_amdgcn_perm(u1, t1, 0x05040100), __builtin_amdgcn_perm(u1, t1, 0x07060302)};
+// The 16 scale bytes of a pass: even blocks, then odd ones.
+__device__ inline v4u split_scales(v4u v) {
+  return v4u{__builtin_amdgcn_perm(v[1], v[0], 0x06040200), __builtin_amdgcn_perm(v[3], v[2], 0x06040200),
+             __builtin_amdgcn_perm(v[1], v[0], 0x07050301), __builtin_amdgcn_perm(v[3], v[2], 0x07050301)};
+}
+
+// The wave's outputs.  Register 4 k + q of lane (r, b), tile (i, c): row 32 i + 8
+// k + 4 b + q of the wave's, column 32 c + r.  Offsets are relative to the
+// item's first row; the view ends with its last one, so rows past it are dropped.
+template <typename C, bool F32, int NSUB, int NS>
+__device__ __forceinline__ void store_tile(const ProductArgs& p, const Item& it, const int* src, int wave,
+                                           v16f (&acc)[NS][C::sn]) {
+  constexpr int kEl = F32 ? 4 : 2;
+  const int lane = threadIdx.x & 63, r = lane & 31, b = lane >> 5;
+  const int n = it.bx * C::BN + 32 * C::sn * (wave % C::nw) + r, m0 = 32 * C::sm * (wave / C::nw) + 4 * b;
+  const Buf out = make_buf(static_cast<const uint8_t*>(p.out) + (size_t)it.row0 * p.N * kEl, (uint32_t)it.rows * p.N * kEl);
+  uint32_t at[C::sn];
+#pragma unroll
+  for (int c = 0; c < C::sn; c++) at[c] = n + 32 * c < p.N ? ((uint32_t)m0 * p.N + n + 32 * c) * kEl : kNowhere;
+  // whether a row of the wave's has its source outside A (its output is zero)
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NSUB; i++) {
+    const int m = m0 - 4 * b + 32 * i + r;
+    bad |= m < it.rows && src[m] < 0;
+  }
+  bad = __any(bad);
+#pragma unroll
+  for (int i = 0; i < NSUB; i++)
+#pragma unroll
+    for (int q = 0; q < 16; q++) {
+      const int dm = 32 * i + 8 * (q / 4) + q % 4, so = dm * p.N * kEl;
+      bool zero = false;
+      if (bad) zero = m0 + dm < it.rows && src[m0 + dm] < 0;
+#pragma unroll
+      for (int c = 0; c < C::sn; c++) {
+        const float v = zero ? 0.0f : acc[i][c][q];
+        if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b32(f_bits(v), out, (int)at[c], so, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), out, (int)at[c], so, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // one row at a time: the accumulators leave no registers for more
+    }
 }
 
 // The tile's work of one wave whose rows fill NSUB of its SM sub-tiles.  Waves
 // of a workgroup may run different NSUB: the barriers are the same in all.
-template <typename C, int NSUB>
+template <typename C, bool F32, int NSUB>
 __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& it, uint8_t* lds, const int* src,
                                              int wave) {
   constexpr int SM = C::sm, SN = C::sn;
@@ -83,156 +134,161 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& i
 #pragma unroll
     for (int i = 0; i < C::PW; i++) s.w[i] = buf16<false>(wq, wo + i * (C::T / 4) * row_bytes);
   };
-  auto store = [&](int slot, const Stage& s) {
-    uint8_t* t = lds + slot * C::kSlot;
+  auto store = [&](uint8_t* t, const Stage& s) {
 #pragma unroll
     for (int i = 0; i < C::PA + C::PW; i++) {
       const int row = lrow + i * (C::T / 4);
       *reinterpret_cast<v4u*>(t + row * 64 + 16 * column(row, lb)) = i < C::PA ? s.a[i] : s.w[i - C::PA];
     }
   };
-  // scales: thread t < BM + BN takes row t (of A, then of W), 16 blocks at a time; past the end of k zeros
-  const uint8_t* scr = p.a_sc;
-  if (tid < C::BM) scr = p.a_sc + (size_t)max(src[tid], 0) * nb;
-  else if (tid < C::BM + C::BN) scr = p.w_sc + (wr0 + min(tid - C::BM, wrows - 1)) * nb;
-  auto load_scales = [&](int q) {
-    v4u v = v4u{0, 0, 0, 0};
+  // scales: thread t takes rows t, t + T .. (of A, then of W), 16 blocks at a time; past the end of k zeros
+  const uint8_t* scr[C::R];
+#pragma unroll
+  for (int i = 0; i < C::R; i++) {
+    const int row = tid + i * C::T;
+    scr[i] = row < C::BM ? p.a_sc + (size_t)max(src[row], 0) * nb
+                         : p.w_sc + (wr0 + min(row - C::BM, wrows - 1)) * nb;
+  }
+  struct Scales {
+    v4u v[C::R];
+  };
+  auto load_scales = [&](int q, Scales& s) {
     const int b0 = 16 * q, left = nb - b0;
     if (left >= 16) {
-      __builtin_memcpy(&v, scr + b0, 16);
+#pragma unroll
+      for (int i = 0; i < C::R; i++) __builtin_memcpy(&s.v[i], scr[i] + b0, 16);
     } else {
-      for (int j = 0; j < left; j++) v[j >> 2] |= (uint32_t)scr[b0 + j] << (8 * (j & 3));
+#pragma unroll
+      for (int i = 0; i < C::R; i++) {
+        s.v[i] = v4u{0, 0, 0, 0};
+        for (int j = 0; j < left; j++) s.v[i][j >> 2] |= (uint32_t)scr[i][b0 + j] << (8 * (j & 3));
+      }
     }
-    return v;
   };
-  uint8_t* const sc_lds = lds + 4 * C::kSlot;
-  auto store_scales = [&](int buf, v4u v) {
-    if (tid < C::BM + C::BN) *reinterpret_cast<v4u*>(sc_lds + buf * C::kScale + 16 * tid) = transpose_bytes(v);
+  uint8_t* const sc_lds = lds + 3 * C::kSlot;
+  auto store_scales = [&](const Scales& s) {
+#pragma unroll
+    for (int i = 0; i < C::R; i++)
+      if (tid + i * C::T < C::BM + C::BN) *reinterpret_cast<v4u*>(sc_lds + 16 * (tid + i * C::T)) = split_scales(s.v[i]);
   };
 
   // multiplying: this wave's rows and columns
-  const int wm = wave / C::nw, wn = wave % C::nw, r = lane & 15, b = lane >> 4;
-  const int nw = n0 + 16 * SN * wn;
-  const int arow = 16 * SM * wm + r, brow = C::BM + 16 * SN * wn + r;   // (a sub-tile is 16 rows: the same columns)
-  const int aoff = arow * 64 + 16 * column(r, b), boff = brow * 64 + 16 * column(r, b);
-  const int asc = arow * 16 + 4 * b, bsc = brow * 16 + 4 * b;
+  const int wm = wave / C::nw, wn = wave % C::nw, r = lane & 31, b = lane >> 5;
+  const int nw = n0 + 32 * SN * wn;
+  const int arow = 32 * SM * wm + r, brow = C::BM + 32 * SN * wn + r;
+  const int aoff[2] = {arow * 64 + 16 * column(r, b), arow * 64 + 16 * column(r, 2 + b)};
+  const int boff[2] = {brow * 64 + 16 * column(r, b), brow * 64 + 16 * column(r, 2 + b)};
+  const int asc = arow * 16 + 8 * b, bsc = brow * 16 + 8 * b;
 
-  v4f acc[NSUB > 0 ? NSUB : 1][SN];
+  v16f acc[NSUB > 0 ? NSUB : 1][SN];
 #pragma unroll
   for (int i = 0; i < NSUB; i++)
 #pragma unroll
-    for (int c = 0; c < SN; c++) acc[i][c] = v4f{0, 0, 0, 0};
+    for (int c = 0; c < SN; c++)
+#pragma unroll
+      for (int q = 0; q < 16; q++) acc[i][c][q] = 0.0f;
 
-  int wsc[SN], asv[NSUB > 0 ? NSUB : 1];                 // scale words of a pass
-  auto compute = [&](auto J) {                           // half step J of a pass, slot J
+  v2u wsc[SN], asv[NSUB > 0 ? NSUB : 1];                 // scale words of a pass
+  auto compute = [&](auto J, const uint8_t* t) {         // half step J of a pass, in slot t
     constexpr int j = decltype(J)::value;
-    const uint8_t* t = lds + j * C::kSlot;
-    v4u w[SN];
 #pragma unroll
-    for (int c = 0; c < SN; c++) w[c] = *reinterpret_cast<const v4u*>(t + boff + 1024 * c);
+    for (int u = 0; u < 2; u++) {
+      v4u w[SN];
 #pragma unroll
-    for (int i = 0; i < NSUB; i++) {
-      const v4u a = *reinterpret_cast<const v4u*>(t + aoff + 1024 * i);
+      for (int c = 0; c < SN; c++) w[c] = *reinterpret_cast<const v4u*>(t + boff[u] + 2048 * c);
 #pragma unroll
-      for (int c = 0; c < SN; c++) acc[i][c] = mma_codes<j>(w[c], wsc[c], a, asv[i], acc[i][c]);
+      for (int i = 0; i < NSUB; i++) {
+        const v4u a = *reinterpret_cast<const v4u*>(t + aoff[u] + 2048 * i);
+#pragma unroll
+        for (int c = 0; c < SN; c++) {
+          if (u == 0) acc[i][c] = mma32<2 * (j & 1)>(a, asv[i][j / 2], w[c], wsc[c][j / 2], acc[i][c]);
+          else acc[i][c] = mma32<2 * (j & 1) + 1>(a, asv[i][j / 2], w[c], wsc[c][j / 2], acc[i][c]);
+        }
+      }
     }
   };
 
   Stage st[2];
   load(0, st[0]);
   load(1, st[1]);
-  v4u sc = load_scales(0);
-  store(0, st[0]);
+  Scales sc;
+  load_scales(0, sc);
+  store(lds, st[0]);
   load(2, st[0]);
-  store(1, st[1]);
+  store(lds + C::kSlot, st[1]);
   load(3, st[1]);
-  store_scales(0, sc);
+  store_scales(sc);
   lds_barrier();
-  // h: 4 half steps per pass, slot and scale byte group h % 4, register set h % 2
-  for (int h0 = 0, sb = 0; h0 < halves; h0 += 4, sb ^= 1) {
-    sc = load_scales(h0 / 4 + 1);
+  int slot = 0, free_slot = 2 * C::kSlot;                // of half steps h and h + 2
+  auto next_slot = [&](int s) { return s == 2 * C::kSlot ? 0 : s + C::kSlot; };
+  // 4 half steps per pass: scale bytes by h % 4, register set h % 2
+  for (int h0 = 0; h0 < halves; h0 += 4) {
     if constexpr (NSUB > 0) {
-      const uint8_t* s = sc_lds + sb * C::kScale;
 #pragma unroll
-      for (int c = 0; c < SN; c++) wsc[c] = *reinterpret_cast<const int*>(s + bsc + 256 * c);
+      for (int c = 0; c < SN; c++) wsc[c] = *reinterpret_cast<const v2u*>(sc_lds + bsc + 512 * c);
 #pragma unroll
-      for (int i = 0; i < NSUB; i++) asv[i] = *reinterpret_cast<const int*>(s + asc + 256 * i);
+      for (int i = 0; i < NSUB; i++) asv[i] = *reinterpret_cast<const v2u*>(sc_lds + asc + 512 * i);
     }
     auto half_step = [&](auto J) {
       constexpr int j = decltype(J)::value;
+      if constexpr (j == 0) load_scales(h0 / 4 + 1, sc);
       if constexpr (NSUB > 0) {
-        if (h0 + j < halves) compute(J);
+        if (h0 + j < halves) compute(J, lds + slot);
       }
-      store((j + 2) & 3, st[j & 1]);                     // half step h0 + j + 2
+      __builtin_amdgcn_sched_barrier(0);                 // (moved up, the loads would need registers of their own)
+      store(lds + free_slot, st[j & 1]);                 // half step h0 + j + 2
+      __builtin_amdgcn_sched_barrier(0);
       load(h0 + j + 4, st[j & 1]);
-      if constexpr (j == 1) lds_barrier();
-      if constexpr (j == 3) {
-        store_scales(sb ^ 1, sc);
-        lds_barrier();
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (j == 3) store_scales(sc);          // the last ones went to registers at the start of the pass
+      lds_barrier();
+      slot = next_slot(slot);
+      free_slot = next_slot(free_slot);
     };
     half_step(std::integral_constant<int, 0>{});
     half_step(std::integral_constant<int, 1>{});
     half_step(std::integral_constant<int, 2>{});
     half_step(std::integral_constant<int, 3>{});
   }
-
-  // register q of lane (r, b), tile (i, c): row 16 i + r of the wave's, column 16 c + 4 b + q
-  const bool wide = p.N % 4 == 0;
-#pragma unroll
-  for (int i = 0; i < NSUB; i++) {
-    const int m = 16 * SM * wm + 16 * i + r;
-    if (m >= it.rows) continue;
-    const bool zero = src[m] < 0;
-#pragma unroll
-    for (int c = 0; c < SN; c++) {
-      const int n = nw + 16 * c + 4 * b;
-      const v4f v = zero ? v4f{0, 0, 0, 0} : acc[i][c];
-      const size_t at = (size_t)(it.row0 + m) * p.N + n;
-      if (wide) {
-        if (n < p.N) store_out4(p, at, v);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-          if (n + q < p.N) store_out(p, at + q, v[q]);
-      }
-    }
-  }
+  store_tile<C, F32, NSUB>(p, it, src, wave, acc);
 }
 
-template <int MW, int NW, int SM, int SN>
-__global__ __launch_bounds__(64 * MW * NW, 2) void k_product_tile(ProductArgs p) {
+template <int MW, int NW, int SM, int SN, bool F32>
+__global__ __launch_bounds__(64 * MW * NW, SM * SN > 4 ? 2 : 4) void k_product_tile(ProductArgs p) {
   typedef Tile<MW, NW, SM, SN> C;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int* const src = reinterpret_cast<int*>(lds + C::kLds);                    // [BM]
   Item it;
-  if (!find_item<C::BM>(p, (p.N + C::BN - 1) / C::BN, it)) return;
+  if (!find_item<C::BM>([&](int i) { return clamped_offset(p, i); }, p.G, (p.N + C::BN - 1) / C::BN, blockIdx.x, it))
+    return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (tid < C::BM) src[tid] = tid < it.rows ? source_row(p, it.row0 + tid) : -1;
   __syncthreads();
   // bodies for fewer rows (a group's last tile is usually partial) leave out
   // the reads and instructions of sub-tiles without rows
-  const int wm = wave / NW, nw = it.bx * C::BN + 16 * SN * (wave % NW);
-  const int rows = nw < p.N ? it.rows - 16 * SM * wm : 0;
-  if (rows <= 0) product_tile<C, 0>(p, it, lds, src, wave);
-  else if (rows <= 4 * SM) product_tile<C, SM / 4>(p, it, lds, src, wave);
-  else if (rows <= 8 * SM) product_tile<C, SM / 2>(p, it, lds, src, wave);
-  else if (rows <= 12 * SM) product_tile<C, 3 * SM / 4>(p, it, lds, src, wave);
-  else product_tile<C, SM>(p, it, lds, src, wave);
+  const int wm = wave / NW, nw = it.bx * C::BN + 32 * SN * (wave % NW);
+  const int rows = nw < p.N ? it.rows - 32 * SM * wm : 0;
+  if (rows <= 0) product_tile<C, F32, 0>(p, it, lds, src, wave);
+  else if (rows <= 32) product_tile<C, F32, 1>(p, it, lds, src, wave);
+  else if (SM == 2 || rows <= 64) product_tile<C, F32, 2>(p, it, lds, src, wave);
+  else if (rows <= 96) product_tile<C, F32, SM - 1>(p, it, lds, src, wave);
+  else product_tile<C, F32, SM>(p, it, lds, src, wave);
 }
 
 template <int MW, int NW, int SM, int SN>
 static void launch_tile(const ProductArgs& p, hipStream_t stream) {
   typedef Tile<MW, NW, SM, SN> C;
   const dim3 grid((unsigned)max_tiles(p, C::BM) * ceil_div(p.N, C::BN));
-  hipLaunchKernelGGL((k_product_tile<MW, NW, SM, SN>), grid, dim3(C::T), C::kLds + 4 * C::BM, stream, p);
+  const size_t bytes = C::kLds + 4 * C::BM;
+  if (p.out_f32) hipLaunchKernelGGL((k_product_tile<MW, NW, SM, SN, true>), grid, dim3(C::T), bytes, stream, p);
+  else hipLaunchKernelGGL((k_product_tile<MW, NW, SM, SN, false>), grid, dim3(C::T), bytes, stream, p);
 }
 
 int launch_product_tile(const ProductArgs& p, hipStream_t stream) {
   // the large tile where it still gives most CUs (256) a workgroup
-  const long tiles = ceil_div(p.M, 256) > p.G ? ceil_div(p.M, 256) : p.G;
-  if (tiles * ceil_div(p.N, 256) >= 192) launch_tile<2, 4, 8, 4>(p, stream);
-  else launch_tile<2, 2, 4, 2>(p, stream);
+  const long tiles = ceil_div(p.M, 128) > p.G ? ceil_div(p.M, 128) : p.G;
+  if (tiles * ceil_div(p.N, 256) >= 192) launch_tile<1, 4, 4, 2>(p, stream);
+  else launch_tile<2, 2, 2, 1>(p, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
