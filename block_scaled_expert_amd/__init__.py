@@ -17,6 +17,7 @@ There is no fallback: if the built library is missing, load() raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -149,9 +150,11 @@ def _ok(status: int, what: str) -> None:
         raise MoeError(status, what)
 
 
-def _stream():
+def _stream() -> int:
+    """The current stream's handle.  The raw accessor: building a Stream object
+    takes 3 us, more than everything else around a small call."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t, dtype=None, shape=None, name="tensor"):
@@ -163,9 +166,9 @@ def _ptr(t, dtype=None, shape=None, name="tensor"):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _code_cols(fmt: str, cols: int) -> int:
@@ -190,6 +193,12 @@ def workspace(cfg: Config, device="cuda"):
     return torch.empty(workspace_size(cfg), dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=None)
+def _default_config(fmt: str):
+    cfg = Config(fmt=fmt)
+    return cfg, cfg.c()
+
+
 def quantize_act(cfg, x, codes, scales, row_gs=None, site: int = 0, ws=None) -> None:
     """NVFP4 / MXFP8 / MXFP4 quantization of a bf16 or fp32 [rows, cols] tensor in
     cfg's format and activation-scale mode (cfg: a Config, or a format name
@@ -198,15 +207,15 @@ def quantize_act(cfg, x, codes, scales, row_gs=None, site: int = 0, ws=None) -> 
     scales."""
     import torch
     if isinstance(cfg, str):
-        cfg = Config(fmt=cfg)
+        cfg, cc = _default_config(cfg)
+    else:
+        cc = cfg.c()
     rows, cols = x.shape
     dt = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(x.dtype)
     if dt is None:
         raise ValueError("x must be bfloat16 or float32")
     nv = cfg.fmt == "nvfp4"
-    _ptr(x, name="x")
-    cc = cfg.c()
-    args = (ctypes.byref(cc), site, dt, _ptr(x), rows, cols,
+    args = (ctypes.byref(cc), site, dt, _ptr(x, name="x"), rows, cols,
             _ptr(codes, torch.uint8, (rows, _code_cols(cfg.fmt, cols)), "codes"),
             _ptr(scales, torch.uint8, (rows, _scale_cols(cfg.fmt, cols)), "scales"),
             _ptr(row_gs, torch.float32, (rows,), "row_gs") if nv else None,

@@ -184,7 +184,7 @@ int check_balance(const moe_config* c, int T, int S) {
   if (c == nullptr) return MOE_ERR_INVALID_ARG;
   if (c->num_experts < 1 || c->num_experts > 1024) return MOE_ERR_INVALID_ARG;
   if (c->top_k < 1 || c->top_k > 32 || c->top_k > c->num_experts) return MOE_ERR_INVALID_ARG;
-  if (T < 0 || T > (1 << 26) || S < 1 || S > 65535) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || T > (1 << 26) || (long)T * c->top_k > (1L << 30) || S < 1 || S > 65535) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 

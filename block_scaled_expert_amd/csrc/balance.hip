@@ -24,79 +24,109 @@ namespace moe {
 
 namespace {
 
+// Sum over the wavefront, the same in every lane: within each row of 16 lanes
+// by DPP (neighbours, pairs, half rows, rows), then the four rows.  A third of
+// the instructions' latency of an exchange through LDS, and one fixed order.
+template <int CTRL>
+__device__ inline float dpp_add(float v) {
+  return v + bits_f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f_bits(v), CTRL, 0xF, 0xF, false));
+}
+__device__ inline float row_sum(float v) {
+  v = dpp_add<0xB1>(v);    // quad_perm [1,0,3,2]
+  v = dpp_add<0x4E>(v);    // quad_perm [2,3,0,1]
+  v = dpp_add<0x141>(v);   // row_half_mirror
+  return dpp_add<0x140>(v);   // row_mirror
+}
+__device__ inline float lane_f(float v, int l) { return bits_f((uint32_t)__builtin_amdgcn_readlane((int)f_bits(v), l)); }
+__device__ inline float all_sum(float v) {
+  v = row_sum(v);
+  return (lane_f(v, 0) + lane_f(v, 16)) + (lane_f(v, 32) + lane_f(v, 48));
+}
+// The same where lanes 32 .. 63 hold zero.
+__device__ inline float half_sum(float v) {
+  v = row_sum(v);
+  return lane_f(v, 0) + lane_f(v, 16);
+}
+
 // e^x for x <= 0, relative error below 2e-7: the hardware's exp2 of x log2(e),
-// with the rounding of that product put back to first order.
+// with the rounding of that product put back to first order.  Below -200 (0 in
+// fp32) as at -200, which keeps -inf out of the products.
 __device__ inline float exp_neg(float x) {
-  x = x < -200.0f ? -200.0f : x;               // e^-200 is 0 in fp32; keeps -inf out of the products
+  x = fmaxf(x, -200.0f);
   const float y = x * 1.44269504f;
   const float r = fmaf(x, 1.44269504f, -y) + x * 1.9259630e-8f;
   const float e = __builtin_amdgcn_exp2f(y);
   return fmaf(e * r, 0.693147181f, e);
 }
 
-// sigmoid(z) * e^-shift as t, and 1 - sigmoid(z) as c, for shift = min(0, max
-// of the row): with shift = 0 the plain sigmoid; a row whose logits are all far
-// below zero keeps its proportions, where the sigmoids themselves underflow.
-// em = e^shift.
-__device__ inline void sig(float z, float shift, float em, float& t, float& c) {
-  const bool pos = z >= 0.0f;
-  const float e = exp_neg(pos ? -z : z - shift);
-  const float r = __builtin_amdgcn_rcpf(1.0f + (pos ? e : e * em));
-  t = pos ? r : e * r;
-  c = pos ? e * r : r;
+// sigmoid(z) as t and 1 - sigmoid(z) as c.  A NaN gives finite values: rows
+// are checked for NaN on their own.
+__device__ inline void sig(float z, float& t, float& c) {
+  const float e = exp_neg(-fabsf(z));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+  t = z >= 0.0f ? r : er;
+  c = z >= 0.0f ? er : r;
+}
+// sigmoid(z) e^-shift and 1 - sigmoid(z) for z <= shift <= 0: a row whose logits
+// are all far below zero keeps its proportions, where the sigmoids themselves
+// underflow.  em = e^shift.
+__device__ inline void sig_shifted(float z, float shift, float em, float& t, float& c) {
+  const float e = exp_neg(z - shift);
+  c = __builtin_amdgcn_rcpf(fmaf(e, em, 1.0f));
+  t = e * c;
 }
 
-template <typename T>
-__device__ inline float load_z(const T* p);
-template <>
-__device__ inline float load_z<float>(const float* p) { return *p; }
-template <>
-__device__ inline float load_z<uint16_t>(const uint16_t* p) { return bf16_to_f32(*p); }
-
+__device__ inline float load_z(const float* p) { return *p; }
+__device__ inline float load_z(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ inline void store_dz(float* p, float v) { *p = v; }
 __device__ inline void store_dz(uint16_t* p, float v) { *reinterpret_cast<__bf16*>(p) = (__bf16)v; }
 
 // A token's row: t[i] proportional to sigmoid(z), c[i] = 1 - sigmoid(z) of
 // expert lane + 64 i (t = 0 past E), and 1 / sum t (0 for a row whose logits
-// are all -inf).
+// are all -inf, NaN if one is NaN).
 template <int NPER>
 struct Row {
   float t[NPER], c[NPER], inv;
-  float shift, em;
 };
 
 template <int NPER>
 __device__ inline void make_row(const float (&z)[NPER], int E, int lane, Row<NPER>& r) {
   float sum = 0.0f;
-  r.shift = 0.0f;
-  r.em = 1.0f;
+  bool nan = false;
 #pragma unroll
   for (int i = 0; i < NPER; i++) {
-    sig(z[i], 0.0f, 1.0f, r.t[i], r.c[i]);
-    if (lane + 64 * i >= E) r.t[i] = 0.0f;
+    const bool in = lane + 64 * i < E;
+    sig(z[i], r.t[i], r.c[i]);
+    r.t[i] = in ? r.t[i] : 0.0f;
+    nan |= z[i] != z[i];                         // (lanes past E repeat the last expert)
     sum += r.t[i];
   }
-  sum = wave_sum(sum);
-  if (sum < 1e-12f) {   // uniform; every logit is below -27: shift by their maximum
+  sum = all_sum(sum);
+  if (sum < 1e-12f) {                            // uniform; every logit is below -27: shift by their maximum
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPER; i++)
-      if (lane + 64 * i < E) m = fmaxf(m, z[i]);
+    for (int i = 0; i < NPER; i++) m = fmaxf(m, z[i]);
     m = wave_max(m);
     sum = 0.0f;
     if (m > -INFINITY) {
-      r.shift = m;
-      r.em = exp_neg(m);
+      const float em = exp_neg(m);
 #pragma unroll
       for (int i = 0; i < NPER; i++) {
-        sig(z[i], m, r.em, r.t[i], r.c[i]);
+        sig_shifted(z[i], m, em, r.t[i], r.c[i]);
         if (lane + 64 * i >= E) r.t[i] = 0.0f;
         sum += r.t[i];
       }
-      sum = wave_sum(sum);
+      sum = all_sum(sum);
     }
   }
-  r.inv = sum == 0.0f ? 0.0f : 1.0f / sum;     // a NaN logit makes the row NaN
+  r.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (__any(nan)) r.inv = __builtin_nanf("");
+}
+
+template <typename ZT, int NPER>
+__device__ inline void load_row(const ZT* z, int E, int lane, float (&v)[NPER]) {
+#pragma unroll
+  for (int i = 0; i < NPER; i++) v[i] = load_z(z + min(lane + 64 * i, E - 1));
 }
 
 // First token of sequence s, clamped to [0, T] whatever the device array holds.
@@ -105,16 +135,19 @@ __device__ inline int bound(const BalanceArgs& a, int s) {
   return min(max(a.bounds[s], 0), a.T);
 }
 
-// The sequence of token t: the largest s with bounds[s] <= t (-1: none).
-__device__ inline int seq_of(const BalanceArgs& a, int t) {
+// The sequence of token t: the largest s with bounds[s] <= t (-1: none).  The
+// wave looks at 64 bounds at a time.
+__device__ inline int seq_of(const BalanceArgs& a, int t, int lane) {
   if (a.bounds == nullptr) return 0;
-  int lo = -1, hi = a.S;                       // bounds[lo] <= t < bounds[hi], read as sentinels at the ends
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (a.bounds[m] <= t) lo = m;
-    else hi = m;
+  int lo = 0, hi = a.S;                          // the number of bounds <= t is in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 63) / 64, at = lo + lane * step;
+    const int n = __popcll(__ballot(at < hi && a.bounds[min(at, a.S)] <= t));
+    if (n == 0) break;
+    hi = min(hi, lo + n * step);
+    lo += (n - 1) * step + 1;
   }
-  return lo;
+  return lo - 1;
 }
 
 // Forward, first launch: workgroup c takes tokens [c C, (c + 1) C) and, for
@@ -132,8 +165,8 @@ struct BalanceWs {
 constexpr int kMaxE = 1024, kFinishCols = kMaxE / 64;
 
 __host__ __device__ inline int balance_chunk(int T) {
-  const int c = (T + 511) / 512;               // about two workgroups per CU
-  return c < 16 ? 16 : c;
+  const int c = (T + 1023) / 1024;             // four workgroups per CU, at least one token a wave
+  return c < 4 ? 4 : c;
 }
 
 template <typename ZT, int NPER>
@@ -141,36 +174,49 @@ __global__ __launch_bounds__(256) void k_balance_part(BalanceArgs a, BalanceWs w
   __shared__ float psum[4][64 * NPER];
   __shared__ int32_t hist[64 * NPER];
   __shared__ int32_t nlive[4];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   if (blockIdx.x == 0)                         // the second launch counts its workgroups here
     for (int s = tid; s < a.S; s += 256) w.ticket[s] = 0;
   const int t0 = blockIdx.x * w.chunk, t1 = min(t0 + w.chunk, a.T);
   const ZT* z = static_cast<const ZT*>(a.z);
-  int s = max(seq_of(a, t0), 0);
+  int s = max(seq_of(a, t0, lane), 0);
   for (; s < a.S; s++) {
     const int lo = max(bound(a, s), t0), hi = min(bound(a, s + 1), t1);
     if (lo >= t1) break;
     if (lo >= hi) continue;
+    // the wave's tokens lo + wave, + 4 ..: the next one's logits are on their way while one is worked on
+    int t = lo + wave;
+    float zr[NPER];
+    bool on = false;
+    if (t < hi) {
+      on = a.mask == nullptr || a.mask[t] != 0;
+      load_row<ZT, NPER>(z + (size_t)t * a.E, a.E, lane, zr);
+    }
     for (int e = tid; e < a.E; e += 256) hist[e] = 0;
     __syncthreads();
+    for (int p = lo * a.k + tid; p < hi * a.k; p += 256) {
+      const int id = a.ids[p];
+      if (id >= 0 && id < a.E && (a.mask == nullptr || a.mask[p / a.k] != 0)) atomicAdd(&hist[id], 1);
+    }
     float acc[NPER];
 #pragma unroll
     for (int i = 0; i < NPER; i++) acc[i] = 0.0f;
     int n = 0;
-    for (int t = lo + wave; t < hi; t += 4) {
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
-      n++;
-      float zr[NPER];
+    for (; t < hi; t += 4) {
+      const int tn = min(t + 4, hi - 1);
+      float zn[NPER];
+      const bool on_next = a.mask == nullptr || a.mask[tn] != 0;
+      load_row<ZT, NPER>(z + (size_t)tn * a.E, a.E, lane, zn);
+      if (on) {
+        n++;
+        Row<NPER> r;
+        make_row<NPER>(zr, a.E, lane, r);
 #pragma unroll
-      for (int i = 0; i < NPER; i++) zr[i] = load_z<ZT>(z + (size_t)t * a.E + min(lane + 64 * i, a.E - 1));
-      if (lane < a.k) {
-        const int id = a.ids[(size_t)t * a.k + lane];
-        if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
+        for (int i = 0; i < NPER; i++) acc[i] = fmaf(r.t[i], r.inv, acc[i]);
       }
-      Row<NPER> r;
-      make_row<NPER>(zr, a.E, lane, r);
+      on = on_next;
 #pragma unroll
-      for (int i = 0; i < NPER; i++) acc[i] = fmaf(r.t[i], r.inv, acc[i]);
+      for (int i = 0; i < NPER; i++) zr[i] = zn[i];
     }
 #pragma unroll
     for (int i = 0; i < NPER; i++) psum[wave][lane + 64 * i] = acc[i];
@@ -198,6 +244,7 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, BalanceW
   const int c0 = lo / w.chunk, c1 = hi > lo ? (hi - 1) / w.chunk + 1 : c0;   // chunks [c0, c1)
   float p = 0.0f;
   int32_t c = 0, n = 0;
+#pragma unroll 8
   for (int i = c0 + wave; i < c1; i += 16) {
     const size_t slot = (size_t)i + s;
     p += w.sums[slot * a.E + ec];
@@ -223,7 +270,7 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, BalanceW
       a.probs[(size_t)s * a.E + e] = p;
       a.counts[(size_t)s * a.E + e] = c;
     }
-    const float part = wave_sum(e < a.E ? (float)c * inv * p : 0.0f);
+    const float part = all_sum(e < a.E ? (float)c * inv * p : 0.0f);
     if (lane == 0) {
       if (blockIdx.x == 0) a.live[s] = n;
       __hip_atomic_store(w.part + s * kFinishCols + blockIdx.x, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -238,90 +285,105 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, BalanceW
   }
 }
 
-// Backward: one wavefront per token, runs of kRun tokens (the counts of a
-// sequence are read again only where the sequence changes).
-constexpr int kRun = 4;
-
+// Backward: one wavefront works through a run of tokens, the next one's logits,
+// ids and weights' gradients on their way while one is worked on.  The counts
+// of a sequence are read where the sequence changes.  The gate weights' share
+// reaches its experts through a row of LDS per wave.
 template <typename ZT, int NPER>
-__global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int t0 = (blockIdx.x * 4 + wave) * kRun;
+__global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a, int run) {
+  __shared__ float gate_row[4][64 * NPER];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int t0 = (blockIdx.x * 4 + wave) * run, t1 = min(t0 + run, a.T);
   const ZT* z = static_cast<const ZT*>(a.z);
   ZT* dz = static_cast<ZT*>(a.dz);
-  float g[NPER];
-  int s = -2, s_hi = t0;                        // tokens below s_hi belong to s
-  bool in_seq = false;
-  for (int t = t0; t < min(t0 + kRun, a.T); t++) {
-    if (t >= s_hi) {
-      s = seq_of(a, t);
-      s_hi = s < 0 ? bound(a, 0) : s < a.S ? bound(a, s + 1) : a.T;
-      in_seq = s >= 0 && s < a.S && t < s_hi;
-      if (s_hi <= t) s_hi = t + 1;              // bounds out of order: look again at the next token
-      const float n = in_seq ? (float)a.live[s] : 0.0f;
-      const float f = n > 0.0f ? a.d_loss[s] * ((float)a.E / ((float)a.k * n)) / n : 0.0f;
+  float* const row = gate_row[wave];
+  if (t0 >= t1) return;                         // no barrier follows
+
+  struct Token {
+    float z[NPER], dw;
+    int id;
+    uint8_t on;
+  };
+  auto load = [&](int t, Token& k) {
+    k.on = a.mask == nullptr ? 1 : a.mask[t];
+    k.id = -1;
+    k.dw = 0.0f;
+    if (a.d_w != nullptr && lane < a.k) {
+      k.id = a.ids[(size_t)t * a.k + lane];
+      k.dw = a.d_w[(size_t)t * a.k + lane];
+    }
+    load_row<ZT, NPER>(z + (size_t)t * a.E, a.E, lane, k.z);
+  };
+  Token cur;
+  load(t0, cur);
 #pragma unroll
-      for (int i = 0; i < NPER; i++)
-        g[i] = in_seq && lane + 64 * i < a.E ? f * (float)a.counts[(size_t)s * a.E + lane + 64 * i] : 0.0f;
+  for (int i = 0; i < NPER; i++) row[lane + 64 * i] = 0.0f;
+
+  float g[NPER];
+  int s_hi = t0;                                // tokens below s_hi belong to the sequence g is of
+  bool in_seq = false;
+  for (int t = t0; t < t1; t++) {
+    Token next;
+    load(min(t + 1, a.T - 1), next);
+    if (t >= s_hi) {
+      const int s = seq_of(a, t, lane);
+      s_hi = s < 0 ? bound(a, 0) : bound(a, s + 1);
+      in_seq = s >= 0 && t < s_hi;
+      if (s_hi <= t) s_hi = t + 1;              // past every sequence, or bounds out of order: look again
+      if (in_seq) {
+        const float n = (float)a.live[s];
+        const float f = n > 0.0f ? a.d_loss[s] * ((float)a.E / ((float)a.k * n)) / n : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPER; i++) g[i] = f * (float)a.counts[(size_t)s * a.E + min(lane + 64 * i, a.E - 1)];
+      }
     }
     ZT* out = dz + (size_t)t * a.E;
-    if (!in_seq || (a.mask != nullptr && a.mask[t] == 0)) {
-#pragma unroll
-      for (int i = 0; i < NPER; i++)
-        if (lane + 64 * i < a.E) store_dz(out + lane + 64 * i, 0.0f);
-      continue;
-    }
-    const ZT* zt = z + (size_t)t * a.E;
-    float zr[NPER];
-#pragma unroll
-    for (int i = 0; i < NPER; i++) zr[i] = load_z<ZT>(zt + min(lane + 64 * i, a.E - 1));
-    Row<NPER> r;
-    make_row<NPER>(zr, a.E, lane, r);
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NPER; i++) dot = fmaf(g[i], r.t[i], dot);
-    dot = wave_sum(dot) * r.inv;
     float d[NPER];
+    if (in_seq && cur.on != 0) {
+      Row<NPER> r;
+      make_row<NPER>(cur.z, a.E, lane, r);
+      float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPER; i++) d[i] = r.t[i] * r.inv * r.c[i] * (g[i] - dot);
-    if (a.d_w != nullptr) {
-      // lane j < k: slot j
-      int id = -1;
-      float v = 0.0f, c = 0.0f, dw = 0.0f;
-      if (lane < a.k) {
-        id = a.ids[(size_t)t * a.k + lane];
-        if (id < 0 || id >= a.E) id = -1;
-        if (id >= 0) dw = a.d_w[(size_t)t * a.k + lane];
-      }
-      const float zs = id >= 0 ? load_z<ZT>(zt + id) : -INFINITY;
-      float gate;
-      sig(zs, 0.0f, 1.0f, v, c);
-      if (a.norm_topk) {
-        float tot = wave_sum(v);
-        if (tot < 1e-12f) {                      // uniform: as in make_row, for the token's slots
-          const float m = wave_max(zs);
-          if (m > -INFINITY) {
-            sig(zs, m, exp_neg(m), v, c);
-            tot = wave_sum(v);
+      for (int i = 0; i < NPER; i++) dot = fmaf(g[i], r.t[i], dot);
+      dot = all_sum(dot) * r.inv;
+#pragma unroll
+      for (int i = 0; i < NPER; i++) d[i] = (r.t[i] * r.inv) * r.c[i] * (g[i] - dot);
+      if (a.d_w != nullptr) {
+        // lane j < k: slot j (k <= 32)
+        const bool in = cur.id >= 0 && cur.id < a.E;
+        const float zs = in ? load_z(z + (size_t)t * a.E + cur.id) : -INFINITY, dw = in ? cur.dw : 0.0f;
+        float v, c;
+        sig(zs, v, c);
+        float gate;
+        if (a.norm_topk) {
+          float tot = half_sum(v);
+          if (tot < 1e-12f) {                   // uniform: as in make_row, for the token's slots
+            const float m = wave_max(zs);
+            if (m > -INFINITY) {
+              sig_shifted(zs, m, exp_neg(m), v, c);
+              tot = half_sum(v);
+            }
           }
+          v = tot == 0.0f ? 0.0f : v / tot;
+          gate = v * c * (dw - half_sum(dw * v));
+        } else {
+          gate = v * c * dw;
         }
-        v = tot == 0.0f ? 0.0f : v / tot;
-        gate = v * c * (dw - wave_sum(dw * v));
-      } else {
-        gate = v * c * dw;
-      }
-      gate *= a.routed_scale;
-      for (int j = 0; j < a.k; j++) {
-        const int idj = __builtin_amdgcn_readlane(id, j);
-        const float gj = bits_f(__builtin_amdgcn_readlane((int)f_bits(gate), j));
-        if (idj < 0) continue;
+        if (in) atomicAdd(&row[cur.id], gate * a.routed_scale);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
 #pragma unroll
-        for (int i = 0; i < NPER; i++)
-          if (idj == lane + 64 * i) d[i] += gj;
+        for (int i = 0; i < NPER; i++) d[i] += row[lane + 64 * i];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        if (in) row[cur.id] = 0.0f;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPER; i++) d[i] = 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < NPER; i++)
       if (lane + 64 * i < a.E) store_dz(out + lane + 64 * i, d[i]);
+    cur = next;
   }
 }
 
@@ -393,13 +455,15 @@ int launch_balance_forward(const BalanceArgs& a, hipStream_t stream) {
 
 int launch_balance_backward(const BalanceArgs& a, hipStream_t stream) {
   if (a.T <= 0) return 0;
-  const dim3 grid(ceil_div(a.T, 4 * kRun));
+  // tokens per wave: 16 waves a CU and then longer runs, up to 16
+  const int want = a.T / 4096, run = want < 1 ? 1 : want > 16 ? 16 : want;
+  const dim3 grid(ceil_div(a.T, 4L * run));
 #define MOE_BACK(N)                                                                                  \
   do {                                                                                               \
     if (a.dtype == 0)                                                                                \
-      hipLaunchKernelGGL((k_balance_backward<uint16_t, N>), grid, dim3(256), 0, stream, a);          \
+      hipLaunchKernelGGL((k_balance_backward<uint16_t, N>), grid, dim3(256), 0, stream, a, run);          \
     else                                                                                             \
-      hipLaunchKernelGGL((k_balance_backward<float, N>), grid, dim3(256), 0, stream, a);             \
+      hipLaunchKernelGGL((k_balance_backward<float, N>), grid, dim3(256), 0, stream, a, run);             \
   } while (0)
   MOE_BAL(MOE_BACK);
 #undef MOE_BACK

@@ -298,14 +298,15 @@ int moe_route_logits(const moe_config* cfg, int32_t T, const void* ws, size_t ws
  *  sequence s holds tokens seq_offsets[s] .. seq_offsets[s+1]-1 (any length,
  *  also none); NULL with S = 1: one sequence of all T tokens.  Tokens
  *  outside every sequence do not count.  token_mask [T] bytes (may be NULL):
- *  tokens with 0 are not live; nothing of them is read.
+ *  tokens with 0 are not live, what their rows hold does not matter.
  *  Outputs: counts [S][E] int32, live [S] int32 (n), probs [S][E], loss [S]
  *  fp32; a sequence without live tokens gives zeros.  Logits may be -inf (an
  *  expert switched off; a row of only -inf has p = 0); a NaN makes its
  *  sequence's probs and loss NaN.
  *  ws: moe_balance_workspace_size bytes of device scratch, 256-byte aligned,
  *  no initial contents needed.  Of cfg only num_experts (at most 1024) and
- *  top_k (at most 32) are read.  T at most 2^26, 1 <= S <= 65535.  Two
+ *  top_k (at most 32) are read.  T at most 2^26, T top_k at most 2^30,
+ *  1 <= S <= 65535.  Two
  *  launches; the same inputs give the same bits. */
 int moe_balance_workspace_size(const moe_config* cfg, int32_t T, int32_t S, size_t* bytes);
 int moe_balance_forward(const moe_config* cfg, int32_t dtype, const void* z, int32_t T, const int32_t* topk_ids,
