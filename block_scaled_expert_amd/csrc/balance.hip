@@ -78,8 +78,15 @@ __device__ inline void sig_shifted(float z, float shift, float em, float& t, flo
 
 __device__ inline float load_z(const float* p) { return *p; }
 __device__ inline float load_z(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ inline void store_dz(float* p, float v) { *p = v; }
-__device__ inline void store_dz(uint16_t* p, float v) { *reinterpret_cast<__bf16*>(p) = (__bf16)v; }
+template <bool NT, typename T>
+__device__ inline void put(T* p, T v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+template <bool NT>
+__device__ inline void store_dz(float* p, float v) { put<NT>(p, v); }
+template <bool NT>
+__device__ inline void store_dz(uint16_t* p, float v) { put<NT>(p, __builtin_bit_cast(uint16_t, (__bf16)v)); }
 
 // A token's row: t[i] proportional to sigmoid(z), c[i] = 1 - sigmoid(z) of
 // expert lane + 64 i (t = 0 past E), and 1 / sum t (0 for a row whose logits
@@ -162,11 +169,13 @@ struct BalanceWs {
   int chunk, nchunks, slots;
 };
 
-constexpr int kMaxE = 1024, kFinishCols = kMaxE / 64;
+constexpr int kMaxE = 1024, kFinishE = 16, kFinishCols = kMaxE / kFinishE;
 
 __host__ __device__ inline int balance_chunk(int T) {
-  const int c = (T + 1023) / 1024;             // four workgroups per CU, at least one token a wave
-  return c < 4 ? 4 : c;
+  // at least a token a wave; four workgroups per CU, eight where they then
+  // still have 16 tokens (each writes E sums and counts)
+  const int c = (T + 1023) / 1024;
+  return c < 4 ? 4 : c <= 16 ? c : c < 32 ? 16 : (T + 2047) / 2048;
 }
 
 template <typename ZT, int NPER>
@@ -232,55 +241,72 @@ __global__ __launch_bounds__(256) void k_balance_part(BalanceArgs a, BalanceWs w
   }
 }
 
-// Forward, second launch: workgroup (x, s) adds the slots of sequence s for 64
-// experts, 16 waves taking every 16th slot; the last of the sequence's
-// workgroups to finish adds their partial losses in order.
+// Forward, second launch: workgroup (x, s) adds the slots of sequence s for
+// kFinishE experts, its groups of 16 lanes (64, or 16 for short sequences)
+// taking the slots in turn; the last of the sequence's workgroups to finish
+// adds their partial losses in order.
 __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, BalanceWs w) {
-  __shared__ float ps[16][64];
-  __shared__ int32_t cs[16][64], ns[16];
+  __shared__ float ps[16][kFinishE];
+  __shared__ int32_t cs[16][kFinishE], ns[16];
   const int s = blockIdx.y, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int e = blockIdx.x * 64 + lane, ec = min(e, a.E - 1);
+  const int e = blockIdx.x * kFinishE + (lane & 15), ec = min(e, a.E - 1);
   const int lo = bound(a, s), hi = bound(a, s + 1);
   const int c0 = lo / w.chunk, c1 = hi > lo ? (hi - 1) / w.chunk + 1 : c0;   // chunks [c0, c1)
   float p = 0.0f;
   int32_t c = 0, n = 0;
 #pragma unroll 8
-  for (int i = c0 + wave; i < c1; i += 16) {
+  for (int i = c0 + (tid >> 4); i < c1; i += (int)blockDim.x / 16) {
     const size_t slot = (size_t)i + s;
     p += w.sums[slot * a.E + ec];
     c += w.counts[slot * a.E + ec];
     n += w.live[slot];
   }
-  ps[wave][lane] = p;
-  cs[wave][lane] = c;
+  // the wave's four groups, then the waves
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1) {
+    p += __shfl_xor(p, o, kWave);
+    c += __shfl_xor(c, o, kWave);
+    n += __shfl_xor(n, o, kWave);
+  }
+  if (lane < kFinishE) {
+    ps[wave][lane] = p;
+    cs[wave][lane] = c;
+  }
   if (lane == 0) ns[wave] = n;
   __syncthreads();
   if (wave == 0) {
     p = 0.0f;
     c = n = 0;
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      p += ps[i][lane];
-      c += cs[i][lane];
+    for (int i = 0; i < (int)blockDim.x / 64; i++) {
+      p += ps[i][lane & 15];
+      c += cs[i][lane & 15];
       n += ns[i];
     }
     const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
     p *= inv;
-    if (e < a.E) {
+    const bool mine = lane < kFinishE && e < a.E;
+    if (mine) {
       a.probs[(size_t)s * a.E + e] = p;
       a.counts[(size_t)s * a.E + e] = c;
     }
-    const float part = all_sum(e < a.E ? (float)c * inv * p : 0.0f);
+    const float part = all_sum(mine ? (float)c * inv * p : 0.0f);
+    int before = 0;
     if (lane == 0) {
       if (blockIdx.x == 0) a.live[s] = n;
+      // device-scope store, complete before the ticket is taken: no cache has to be written back
       __hip_atomic_store(w.part + s * kFinishCols + blockIdx.x, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      const int before = __hip_atomic_fetch_add(w.ticket + s, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-      if (before == (int)gridDim.x - 1) {
-        float l = 0.0f;
-        for (int x = 0; x < (int)gridDim.x; x++)
-          l += __hip_atomic_load(w.part + s * kFinishCols + x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        a.loss[s] = l * ((float)a.E / (float)a.k);
-      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+      asm volatile("" ::: "memory");
+      before = __hip_atomic_fetch_add(w.ticket + s, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(before) == (int)gridDim.x - 1) {
+      asm volatile("" ::: "memory");
+      float l = 0.0f;
+      if (lane < (int)gridDim.x)            // at most kFinishCols = 64
+        l = __hip_atomic_load(w.part + s * kFinishCols + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      l = all_sum(l);
+      if (lane == 0) a.loss[s] = l * ((float)a.E / (float)a.k);
     }
   }
 }
@@ -289,7 +315,7 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, BalanceW
 // ids and weights' gradients on their way while one is worked on.  The counts
 // of a sequence are read where the sequence changes.  The gate weights' share
 // reaches its experts through a row of LDS per wave.
-template <typename ZT, int NPER>
+template <typename ZT, int NPER, bool NT>
 __global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a, int run) {
   __shared__ float gate_row[4][64 * NPER];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -382,7 +408,7 @@ __global__ __launch_bounds__(256) void k_balance_backward(BalanceArgs a, int run
     }
 #pragma unroll
     for (int i = 0; i < NPER; i++)
-      if (lane + 64 * i < a.E) store_dz(out + lane + 64 * i, d[i]);
+      if (lane + 64 * i < a.E) store_dz<NT>(out + lane + 64 * i, d[i]);
     cur = next;
   }
 }
@@ -449,24 +475,32 @@ int launch_balance_forward(const BalanceArgs& a, hipStream_t stream) {
   } while (0)
   MOE_BAL(MOE_PART);
 #undef MOE_PART
-  hipLaunchKernelGGL(k_balance_finish, dim3(ceil_div(a.E, 64), a.S), dim3(1024), 0, stream, a, w);
+  hipLaunchKernelGGL(k_balance_finish, dim3(ceil_div(a.E, kFinishE), a.S), dim3(w.nchunks > 64 * a.S ? 1024 : 256), 0,
+                     stream, a, w);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_balance_backward(const BalanceArgs& a, hipStream_t stream) {
   if (a.T <= 0) return 0;
-  // tokens per wave: 16 waves a CU and then longer runs, up to 16
-  const int want = a.T / 4096, run = want < 1 ? 1 : want > 16 ? 16 : want;
+  // tokens per wave: 32 waves a CU and then longer runs, up to 16
+  const int want = a.T / 8192, run = want < 1 ? 1 : want > 16 ? 16 : want;
   const dim3 grid(ceil_div(a.T, 4L * run));
-#define MOE_BACK(N)                                                                                  \
-  do {                                                                                               \
-    if (a.dtype == 0)                                                                                \
-      hipLaunchKernelGGL((k_balance_backward<uint16_t, N>), grid, dim3(256), 0, stream, a, run);          \
-    else                                                                                             \
-      hipLaunchKernelGGL((k_balance_backward<float, N>), grid, dim3(256), 0, stream, a, run);             \
+  // logits and gradient beyond the last-level cache: the gradient streams past it (161 -> 145 us for a
+  // step over 131072 x 384, whose logits the cache then still holds from the forward)
+  const bool nt = 2 * (size_t)a.T * a.E * (a.dtype == 0 ? 2 : 4) > kStreamBytes;
+#define MOE_BACK_T(ZT, N)                                                                                \
+  do {                                                                                                   \
+    if (nt) hipLaunchKernelGGL((k_balance_backward<ZT, N, true>), grid, dim3(256), 0, stream, a, run);   \
+    else hipLaunchKernelGGL((k_balance_backward<ZT, N, false>), grid, dim3(256), 0, stream, a, run);     \
+  } while (0)
+#define MOE_BACK(N)                        \
+  do {                                     \
+    if (a.dtype == 0) MOE_BACK_T(uint16_t, N); \
+    else MOE_BACK_T(float, N);             \
   } while (0)
   MOE_BAL(MOE_BACK);
 #undef MOE_BACK
+#undef MOE_BACK_T
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 #undef MOE_BAL
