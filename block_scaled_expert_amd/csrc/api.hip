@@ -469,6 +469,7 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
   p.row_ids = row_ids;
   p.id_div = id_div;
   p.M = M;
+  p.expect = M;
   p.w = w;
   p.w_sc = w_scales;
   p.G = G;
@@ -617,6 +618,7 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
     gp.row_ids = b.sorted;
     gp.id_div = k;
     gp.M = P;
+    gp.expect = (int)((long)P * EL / c->num_experts);   // of the pairs, those of local experts
     gp.w = w->w13;
     gp.w_sc = w->w13_sc;
     gp.G = EL;

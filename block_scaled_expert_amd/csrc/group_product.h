@@ -60,13 +60,6 @@ __device__ inline v4f mma4(const Frag& a, const Frag& b, v4f c) {
   // 4, 4: both operands E2M1; J: the scale registers' byte
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, (int)a.sc, J, (int)b.sc);
 }
-// The same from codes and scale words as they are.
-template <int J>
-__device__ inline v4f mma_codes(v4u a, int asc, v4u b, int bsc, v4f c) {
-  const v8i av = v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const v8i bv = v8i{(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, J, asc, J, bsc);
-}
 
 // One chunk of 16 weight rows as loaded: lane (r, b) = (l % 16, l / 16) holds
 // block 2 b + r / 8 of row r % 8 in q[0] and of row 8 + r % 8 in q[1]; sc is
@@ -206,13 +199,6 @@ __device__ inline int source_row(const ProductArgs& p, int r) {
 __device__ inline void store_out(const ProductArgs& p, size_t i, float v) {
   if (p.out_f32) static_cast<float*>(p.out)[i] = v;
   else static_cast<__bf16*>(p.out)[i] = (__bf16)v;   // to nearest even; inf and NaN kept
-}
-
-// Four consecutive columns, i a multiple of 4.
-__device__ inline void store_out4(const ProductArgs& p, size_t i, v4f v) {
-  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-  if (p.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + i) = v;
-  else *reinterpret_cast<v4bf*>(static_cast<__bf16*>(p.out) + i) = __builtin_convertvector(v, v4bf);
 }
 
 }  // namespace moe

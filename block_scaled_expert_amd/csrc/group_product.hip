@@ -164,8 +164,8 @@ static void launch_stream(const ProductArgs& p, hipStream_t stream) {
 int launch_group_product(const ProductArgs& p, hipStream_t stream) {
   if (p.M <= 0) return 0;
   // rows per workgroup from the mean group: 16, 32, and above 48 the tiled kernel
-  if ((long)p.M > 48L * p.G) return launch_product_tile(p, stream);
-  if ((long)p.M <= 16L * p.G) launch_stream<1, 6>(p, stream);
+  if ((long)p.expect > 48L * p.G) return launch_product_tile(p, stream);
+  if ((long)p.expect <= 16L * p.G) launch_stream<1, 6>(p, stream);
   else launch_stream<2, 4>(p, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }

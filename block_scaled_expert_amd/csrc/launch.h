@@ -122,6 +122,7 @@ struct ProductArgs {
   const int32_t* row_ids;   // nullable: row r reads A row row_ids[r] / id_div
   int id_div;
   int M;                    // rows of out
+  int expect;               // rows that the groups are expected to hold, at most M: what the kernel is chosen by
   const uint8_t* w;         // [G][N][K/2], [G][N][K/32]
   const uint8_t* w_sc;
   int G, N, K;
