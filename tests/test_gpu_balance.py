@@ -235,3 +235,36 @@ def test_binding_refusals(gpu_lib):
     assert e.value.status == -3
     with pytest.raises(ValueError):
         gpu_lib.balance_backward(cfg, z, ids, counts, live, loss, z.bfloat16())
+
+
+# sizes on both sides of the one-launch forward's bounds (128 tokens; tokens
+# times groups of 64 experts up to 384), sequences of unequal length in each
+@pytest.mark.parametrize("T,E,k", [(64, 384, 8), (65, 384, 8), (24, 1024, 16), (25, 1024, 16), (128, 192, 4),
+                                   (129, 64, 4), (2, 1024, 32)])
+def test_few_and_more_tokens(gpu_lib, T, E, k):
+    z, ids, d_w = _inputs(T * 3 + E, T, E, k)
+    mask = (np.arange(T) % 5 != 3).astype(np.uint8)
+    for bounds in (None, [0, 0, 1, T - 1, T], [1, 1, T]):
+        _check(_call(gpu_lib, z, ids, E, k, bounds=bounds, mask=mask, d_w=d_w), z, ids, E, k, bounds=bounds,
+               mask=mask, d_w=d_w)
+
+
+def test_extremes_among_many_tokens(gpu_lib):
+    """The extreme rows where the forward takes two launches: repeated over
+    160 tokens, and a NaN that stays in its sequence."""
+    E, k = 100, 4
+    z, ids, d_w = _inputs(12, 160, E, k)
+    z[0::16, ::3] = -np.inf
+    z[1::16] -= 60.0
+    z[2::16] -= 300.0
+    z[3::16] += 60.0
+    z[4::16, 5] = np.inf
+    z[5::16] = -np.inf
+    z[6::16] = np.where(np.arange(E) == 3, -40.0, -np.inf)
+    z[7::16] = np.linspace(-3.0e38, -1.0e38, E)
+    z[8::16] = -28.0
+    _check(_call(gpu_lib, z, ids, E, k, d_w=d_w), z, ids, E, k, d_w=d_w)
+    z[20, 4] = np.nan
+    got = _call(gpu_lib, z, ids, E, k, bounds=[0, 80, 160], d_w=d_w)
+    assert np.isnan(got["loss"][0]) and np.isfinite(got["loss"][1])
+    assert np.isnan(got["dz"][20]).all() and np.isfinite(np.delete(got["dz"], 20, 0)).all()
