@@ -11,18 +11,20 @@
 // 64-byte piece.  So the loads take a half step (k 128, 64 bytes) of 16 rows per
 // wave, row after row, and LDS does the rearrangement.
 //
-// Pipeline, in half steps h: loads of h + 4 go to registers (ring of 2), h + 2
-// goes from there to LDS (3 slots), h is multiplied; one barrier a half step.
-// Scales: 16 bytes (4 half steps, a pass) of a row per load, turned so that a
-// lane's 8 bytes are two words whose bytes the instructions select.  The large
-// tile is 4 waves of 128 x 64 (246 registers, 78 KiB of LDS), so that two
-// workgroups share a CU and one multiplies while the other starts, ends or waits.
+// Pipeline, in half steps h: h + 2 is loaded straight to LDS (3 slots) while h
+// is multiplied; one barrier a half step, passed with the youngest half step's
+// loads still on their way.  Scales: 16 bytes (4 half steps, a pass) of a row
+// per load, through registers, turned so that a lane's 8 bytes are two words
+// whose bytes the instructions select.  The large tile is 4 waves of 128 x 64
+// (199 registers, 78 KiB of LDS), so that two workgroups share a CU and one
+// multiplies while the other starts, ends or waits.
 //
-// Measured (48 groups, 16384 rows x 4608 x 4608, bf16 out): 309 us, 2.25
-// PFLOP/s.  About 213 us are LDS reads and matrix instructions, which the half
-// step's barrier keeps from overlapping fully; storing the outputs takes about
-// 29, the scales' loads 20, waiting for memory 16.  256 x 256 tiles of 8 waves
-// on the 16x16x128 form take 313.
+// Measured (48 groups, 16384 rows x 4608 x 4608, bf16 out): 293 us, 2.37
+// PFLOP/s; with the operands going to LDS through registers, two half steps
+// further ahead, 307; 256 x 256 tiles of 8 waves on the 16x16x128 form 313.
+// What bounds it is LDS: 48 KiB read and 24 written per half step and
+// workgroup, about as long as the matrix instructions, and what the barrier
+// keeps from overlapping.
 //
 // The rows of A are the instruction's first operand and the weights its second,
 // so 32 lanes of a store hold consecutive columns of one row of out: 2 cache
@@ -40,6 +42,18 @@ constexpr int kHalf = 4;                 // blocks of a half step
 // 16-byte column of LDS that holds block b of row `row` (rows of 64 bytes): the
 // operand's 32 rows read at 110 bytes per clock this way, at 67 in plain order.
 __device__ inline int column(int row, int b) { return b ^ ((row >> 2) & 3); }
+
+typedef __attribute__((address_space(3))) uint8_t Lds;
+typedef __attribute__((address_space(1))) uint8_t Glb;
+
+// A barrier after which all but the N youngest loads of every wave have arrived.
+template <int N>
+__device__ inline void loads_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);   // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef unsigned v2u __attribute__((ext_vector_type(2)));
@@ -122,31 +136,25 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& i
   const size_t wr0 = (size_t)it.g * p.N + n0;
   const Buf wq = make_buf(p.w + wr0 * row_bytes, wrows * row_bytes);         // rows past N read zeros
 
-  // loading: thread t takes piece t % 4 of rows t / 4 + i T / 4; rows of A past
-  // the tile repeat its first row (their outputs are not stored)
-  const int lrow = tid >> 2, lb = tid & 3;
+  // loading, straight to LDS: a wave's load fills 1 KiB, 16 rows of 64 bytes, so
+  // the lane's place says which block it takes.  Rows of A past the tile repeat
+  // its first row (their outputs are not stored)
+  const int lrow = tid >> 2, lb = column(tid >> 2, tid & 3);
   const uint8_t* aq[C::PA];
 #pragma unroll
   for (int i = 0; i < C::PA; i++) aq[i] = p.a + (size_t)max(src[lrow + i * (C::T / 4)], 0) * row_bytes;
   const uint32_t woff = lrow * row_bytes;
-  struct Stage {
-    v4u a[C::PA], w[C::PW];
-  };
-  auto load = [&](int h, Stage& s) {
+  auto load = [&](int h, int slot) {
     const int blk = kHalf * h + lb;
     const size_t ao = 16 * (size_t)min(blk, nb - 1);     // past the end of k: any codes, the weights are zero there
     const uint32_t wo = blk < nb ? woff + 16 * blk : kNowhere;
+    Lds* const dst = (Lds*)(lds + slot + wave * 1024);
 #pragma unroll
-    for (int i = 0; i < C::PA; i++) s.a[i] = *reinterpret_cast<const v4u*>(aq[i] + ao);
+    for (int i = 0; i < C::PA; i++) __builtin_amdgcn_global_load_lds((const Glb*)(aq[i] + ao), dst + i * C::T * 16, 16, 0, 0);
 #pragma unroll
-    for (int i = 0; i < C::PW; i++) s.w[i] = buf16<false>(wq, wo + i * (C::T / 4) * row_bytes);
-  };
-  auto store = [&](uint8_t* t, const Stage& s) {
-#pragma unroll
-    for (int i = 0; i < C::PA + C::PW; i++) {
-      const int row = lrow + i * (C::T / 4);
-      *reinterpret_cast<v4u*>(t + row * 64 + 16 * column(row, lb)) = i < C::PA ? s.a[i] : s.w[i - C::PA];
-    }
+    for (int i = 0; i < C::PW; i++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wq, dst + (C::PA + i) * C::T * 16, 16,
+                                               (int)(wo + i * (C::T / 4) * row_bytes), 0, 0, 0);
   };
   // scales: thread t takes rows t, t + T .. (of A, then of W), 16 blocks at a time; past the end of k zeros
   const uint8_t* scr[C::R];
@@ -215,17 +223,12 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& i
     }
   };
 
-  Stage st[2];
-  load(0, st[0]);
-  load(1, st[1]);
   Scales sc;
   load_scales(0, sc);
-  store(lds, st[0]);
-  load(2, st[0]);
-  store(lds + C::kSlot, st[1]);
-  load(3, st[1]);
+  load(0, 0);
   store_scales(sc);
-  lds_barrier();
+  load(1, C::kSlot);
+  loads_barrier<C::PA + C::PW>();
   int slot = 0, free_slot = 2 * C::kSlot;                // of half steps h and h + 2
   auto next_slot = [&](int s) { return s == 2 * C::kSlot ? 0 : s + C::kSlot; };
   // 4 half steps per pass: scale bytes by h % 4, register set h % 2
@@ -239,16 +242,12 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& i
     auto half_step = [&](auto J) {
       constexpr int j = decltype(J)::value;
       if constexpr (j == 0) load_scales(h0 / 4 + 1, sc);
+      if constexpr (j == 3) store_scales(sc);            // read at the start of the pass
+      load(h0 + j + 2, free_slot);
       if constexpr (NSUB > 0) {
         if (h0 + j < halves) compute(J, lds + slot);
       }
-      __builtin_amdgcn_sched_barrier(0);                 // (moved up, the loads would need registers of their own)
-      store(lds + free_slot, st[j & 1]);                 // half step h0 + j + 2
-      __builtin_amdgcn_sched_barrier(0);
-      load(h0 + j + 4, st[j & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (j == 3) store_scales(sc);          // the last ones went to registers at the start of the pass
-      lds_barrier();
+      loads_barrier<C::PA + C::PW>();                     // half step h0 + j + 1 is in LDS
       slot = next_slot(slot);
       free_slot = next_slot(free_slot);
     };
@@ -257,6 +256,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& i
     half_step(std::integral_constant<int, 2>{});
     half_step(std::integral_constant<int, 3>{});
   }
+  loads_barrier<0>();                                      // none may still be on its way when the LDS is given up
   store_tile<C, F32, NSUB>(p, it, src, wave, acc);
 }
 
