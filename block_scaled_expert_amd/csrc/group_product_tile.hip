@@ -243,10 +243,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& i
       constexpr int j = decltype(J)::value;
       if constexpr (j == 0) load_scales(h0 / 4 + 1, sc);
       if constexpr (j == 3) store_scales(sc);            // read at the start of the pass
-      load(h0 + j + 2, free_slot);
       if constexpr (NSUB > 0) {
         if (h0 + j < halves) compute(J, lds + slot);
       }
+      load(h0 + j + 2, free_slot);
       loads_barrier<C::PA + C::PW>();                     // half step h0 + j + 1 is in LDS
       slot = next_slot(slot);
       free_slot = next_slot(free_slot);
