@@ -1,7 +1,7 @@
 // Grouped MXFP4 product, few rows per group (decode, ragged calls): the time
 // is that of streaming the weights of the groups that have rows.
 //
-// Work: one workgroup of 4 waves per (group, 16 MS of its rows, run of NT tiles
+// Work: one workgroup of 4 waves per (group, 16 of its rows, run of NT tiles
 // of 64 weight rows); a wave takes 16 rows of each tile over the whole of k.  Each weight
 // byte is loaded once, by the wave that uses it, into registers (no LDS on
 // that path) through a ring of PF chunks that runs on from tile to tile.  The
@@ -18,21 +18,18 @@ namespace moe {
 
 constexpr int kPanel = 18;   // chunks of A in LDS at a time (k 4608; 39 KiB per 16 rows)
 
-template <int MS>
-constexpr size_t stream_lds(int panel) {
-  return (size_t)MS * panel * (1024 * kU + 64 * 2) + 16 * MS * 4;
-}
+constexpr int kStreamRows = 16;
+constexpr size_t stream_lds(int panel) { return (size_t)panel * (1024 * kU + 64 * 2) + kStreamRows * 4; }
 
-template <int MS, int PF, bool ODD>
+template <int PF, bool ODD>
 __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int panel, int NT) {
-  constexpr int TM = 16 * MS;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  v4u* const lq = reinterpret_cast<v4u*>(lds);                                     // [panel][MS][kU][64]
-  uint16_t* const ls = reinterpret_cast<uint16_t*>(lds + (size_t)panel * MS * kU * 1024);   // [panel][MS][64]
-  int* const src = reinterpret_cast<int*>(ls + (size_t)panel * MS * 64);           // [TM]
+  v4u* const lq = reinterpret_cast<v4u*>(lds);                                     // [panel][kU][64]
+  uint16_t* const ls = reinterpret_cast<uint16_t*>(lds + (size_t)panel * kU * 1024);   // [panel][64]
+  int* const src = reinterpret_cast<int*>(ls + (size_t)panel * 64);                // [kStreamRows]
 
   Item it;
-  if (!find_item<TM>([&](int i) { return clamped_offset(p, i); }, p.G, (p.N + 64 * NT - 1) / (64 * NT), blockIdx.x, it))
+  if (!find_item<kStreamRows>([&](int i) { return clamped_offset(p, i); }, p.G, (p.N + 64 * NT - 1) / (64 * NT), blockIdx.x, it))
     return;
   const int g = it.g, m0 = it.row0, rows = it.rows, n0 = it.bx * 64 * NT;
 
@@ -55,7 +52,7 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
     load_raw<ODD, true>(W, wq, ws, wl, t < tiles, (uint32_t)t * (64 * row_bytes), (uint32_t)t * (64 * nb), c);
   };
 
-  if (tid < TM) src[tid] = tid < rows ? source_row(p, m0 + tid) : -1;
+  if (tid < kStreamRows) src[tid] = tid < rows ? source_row(p, m0 + tid) : -1;
   // the first weights are on their way while the rows of A are fetched
   RawW fw[PF];
   int lt = 0, lc = 0;                               // the chunk that is loaded next
@@ -85,9 +82,9 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
         sv = p.a_sc[(size_t)s * nb + blk];
       }
       // block x of the panel: chunk x / 8, lane group (x % 8) / 2, instruction x % 2
-      const int c = x / kChunkBlocks, slot = c * MS + (row >> 4), l = (row & 15) + 16 * (x % kChunkBlocks / kU);
-      lq[(slot * kU + x % kU) * 64 + l] = v;
-      reinterpret_cast<uint8_t*>(ls + slot * 64 + l)[x % kU] = sv;
+      const int c = x / kChunkBlocks, l = row + 16 * (x % kChunkBlocks / kU);
+      lq[(c * kU + x % kU) * 64 + l] = v;
+      reinterpret_cast<uint8_t*>(ls + c * 64 + l)[x % kU] = sv;
     }
   };
   lds_barrier();                                    // src is written
@@ -97,9 +94,7 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
     lds_barrier();
   }
 
-  v4f acc[MS];
-#pragma unroll
-  for (int i = 0; i < MS; i++) acc[i] = v4f{0, 0, 0, 0};
+  v4f acc = v4f{0, 0, 0, 0};
   int t = 0, c = 0, pc = 0;                         // tile, chunk, chunk within the panel
   while (t < tiles) {
 #pragma unroll
@@ -110,31 +105,22 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
           stage_a(c, min(panel, chunks - c));
           lds_barrier();
         }
-        Frag A[MS], W;
+        Frag A, W;
         operand_w<ODD>(fw[j], W);
 #pragma unroll
-        for (int i = 0; i < MS; i++) {
-#pragma unroll
-          for (int u = 0; u < kU; u++) A[i].q[u] = lq[((pc * MS + i) * kU + u) * 64 + lane];
-          A[i].sc = ls[(pc * MS + i) * 64 + lane];
-        }
-#pragma unroll
-        for (int i = 0; i < MS; i++) acc[i] = mma4<0>(A[i], W, acc[i]);
-#pragma unroll
-        for (int i = 0; i < MS; i++) acc[i] = mma4<1>(A[i], W, acc[i]);
+        for (int u = 0; u < kU; u++) A.q[u] = lq[(pc * kU + u) * 64 + lane];
+        A.sc = ls[pc * 64 + lane];
+        acc = mma4<0>(A, W, acc);
+        acc = mma4<1>(A, W, acc);
         pc = pc + 1 == panel ? 0 : pc + 1;
         if (++c == chunks) {                        // the tile is done
           const int n = nw + 64 * t + r;
 #pragma unroll
-          for (int i = 0; i < MS; i++) {
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-              const int m = 16 * i + 4 * b + q;
-              if (m < rows && n < p.N)
-                store_out(p, (size_t)(m0 + m) * p.N + n, src[m] < 0 ? 0.0f : acc[i][q]);
-            }
-            acc[i] = v4f{0, 0, 0, 0};
+          for (int q = 0; q < 4; q++) {
+            const int m = 4 * b + q;
+            if (m < rows && n < p.N) store_out(p, (size_t)(m0 + m) * p.N + n, src[m] < 0 ? 0.0f : acc[q]);
           }
+          acc = v4f{0, 0, 0, 0};
           c = pc = 0;
           t++;
         }
@@ -145,28 +131,32 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
 }
 
 // Tiles of 64 weight rows per workgroup.
-static int stream_tiles(const ProductArgs& p, int tm) {
-  const long nt = (long)ceil_div(p.N, 64) * max_tiles(p, tm) / 4096;
+static int stream_tiles(const ProductArgs& p) {
+  const long nt = (long)ceil_div(p.N, 64) * max_tiles(p, kStreamRows) / 4096;
   return (int)(nt < 1 ? 1 : nt > 4 ? 4 : nt);
 }
 
-template <int MS, int PF>
 static void launch_stream(const ProductArgs& p, hipStream_t stream) {
-  const int chunks = ceil_div(p.K, kChunkK), panel = chunks < kPanel ? chunks : kPanel;
-  const int tiles = max_tiles(p, 16 * MS), nt = stream_tiles(p, 16 * MS);
-  const dim3 grid((unsigned)tiles * ceil_div(p.N, 64 * nt));
+  constexpr int PF = 6;
+  const int chunks = ceil_div(p.K, kChunkK), panel = chunks < kPanel ? chunks : kPanel, nt = stream_tiles(p);
+  const dim3 grid((unsigned)max_tiles(p, kStreamRows) * ceil_div(p.N, 64 * nt));
   if ((p.K / 32) % 2)
-    hipLaunchKernelGGL((k_product_stream<MS, PF, true>), grid, dim3(256), stream_lds<MS>(panel), stream, p, panel, nt);
+    hipLaunchKernelGGL((k_product_stream<PF, true>), grid, dim3(256), stream_lds(panel), stream, p, panel, nt);
   else
-    hipLaunchKernelGGL((k_product_stream<MS, PF, false>), grid, dim3(256), stream_lds<MS>(panel), stream, p, panel, nt);
+    hipLaunchKernelGGL((k_product_stream<PF, false>), grid, dim3(256), stream_lds(panel), stream, p, panel, nt);
 }
 
+// By the mean group.  At few rows the time is the weights' and they come in
+// faster without LDS and its barriers; a group past 16 rows streams them twice.
+// us, streamed / tiled, for a mean of 1, 4, 8, 12, 16 and 32 rows (random
+// sizes): 384 groups of 4608 x 4608 458/522, 745/828, 814/865, 932/886,
+// 1215/911, 1284/952; 48 of them 65/88, 101/121, 107/123, 127/123, 165/124,
+// 205/130; 384 of 4608 x 2304 214/286, 358/449, 409/461, 458/466, 599/476,
+// 642/505.
 int launch_group_product(const ProductArgs& p, hipStream_t stream) {
   if (p.M <= 0) return 0;
-  // rows per workgroup from the mean group: 16, 32, and above 48 the tiled kernel
-  if ((long)p.expect > 48L * p.G) return launch_product_tile(p, stream);
-  if ((long)p.expect <= 16L * p.G) launch_stream<1, 6>(p, stream);
-  else launch_stream<2, 4>(p, stream);
+  if ((long)p.expect > 10L * p.G) return launch_product_tile(p, stream);
+  launch_stream(p, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

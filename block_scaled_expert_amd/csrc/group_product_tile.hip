@@ -19,12 +19,14 @@
 // (199 registers, 78 KiB of LDS), so that two workgroups share a CU and one
 // multiplies while the other starts, ends or waits.
 //
-// Measured (48 groups, 16384 rows x 4608 x 4608, bf16 out): 293 us, 2.37
-// PFLOP/s; with the operands going to LDS through registers, two half steps
-// further ahead, 307; 256 x 256 tiles of 8 waves on the 16x16x128 form 313.
-// What bounds it is LDS: 48 KiB read and 24 written per half step and
-// workgroup, about as long as the matrix instructions, and what the barrier
-// keeps from overlapping.
+// Measured (48 groups, 16384 rows x 4608 x 4608, bf16 out): 292 us, 2.4
+// PFLOP/s; with the operands going to LDS through registers 307; 256 x 256
+// tiles of 8 waves 293, 128 x 128 of 4 335; with the weights brought to operand
+// order in registers instead of through LDS 310.  No unit is near its rate.
+// Without the loads it takes 184, with loads that all hit a cache 251, without
+// the products 274, without the outputs 269, without the scales 278: the parts
+// of a half step overlap little, and two workgroups a CU, all that registers
+// and LDS hold, do not fill the gaps.
 //
 // The rows of A are the instruction's first operand and the weights its second,
 // so 32 lanes of a store hold consecutive columns of one row of out: 2 cache
@@ -292,7 +294,8 @@ static void launch_tile(const ProductArgs& p, hipStream_t stream) {
 }
 
 int launch_product_tile(const ProductArgs& p, hipStream_t stream) {
-  // the large tile where it still gives most CUs (256) a workgroup
+  // the large tile where it still gives most CUs (256) a workgroup: one group of N 4608, K 4608, us large /
+  // small: 512 rows 26/19, 1024 28/31, 2048 45/51, 4096 72/95
   const long tiles = ceil_div(p.M, 128) > p.G ? ceil_div(p.M, 128) : p.G;
   if (tiles * ceil_div(p.N, 256) >= 192) launch_tile<1, 4, 4, 2>(p, stream);
   else launch_tile<2, 2, 2, 1>(p, stream);

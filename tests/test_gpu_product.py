@@ -197,3 +197,13 @@ def test_binding_refusals(gpu_lib):
     assert e.value.status == -5
     with pytest.raises(gpu_lib.MoeError):
         gpu_lib.group_product(*ok, row_ids=torch.zeros(4, dtype=torch.int32, device="cuda"), id_div=0)
+
+
+@pytest.mark.parametrize("out_f32", [True, False])
+@pytest.mark.parametrize("G,M,N,K,kind", [(2, 20, 80, 256, "even"), (2, 21, 80, 256, "even"), (40, 400, 300, 1184, "uneven"),
+                                          (40, 401, 300, 1184, "uneven"), (9, 90, 640, 4736, "one"),
+                                          (24, 700, 1300, 480, "uneven"), (6, 90, 257, 32, "even")])
+def test_mean_group_of_ten(gpu_lib, G, M, N, K, kind, out_f32):
+    """Both sides of the streaming kernel's bound, with groups of more and of
+    fewer rows than either kernel's tile."""
+    test_product(gpu_lib, G, M, N, K, kind, out_f32)
