@@ -2,8 +2,8 @@
 // is that of streaming the weights of the groups that have rows.
 //
 // Work: one workgroup of 4 waves per (group, 16 of its rows, run of NT tiles
-// of 64 weight rows); a wave takes 16 rows of each tile over the whole of k.  Each weight
-// byte is loaded once, by the wave that uses it, into registers (no LDS on
+// of 64 weight rows); a wave takes 16 rows of each tile over the whole of k.
+// Each weight byte is loaded once, by the wave that uses it, into registers (no LDS on
 // that path) through a ring of PF chunks that runs on from tile to tile.  The
 // operand wants 64 bytes of each of 16 rows; loaded that way every 128-byte
 // line is asked for twice, and the second time it is often gone.  Each load
@@ -12,6 +12,11 @@
 // are staged in LDS in operand order once for all tiles.  Sums over k stay in
 // one accumulator in k order, so a result depends on nothing but its own
 // operands.
+//
+// Measured: 512 rows over 283 of 384 groups of 4608 x 4608, 559 us (5.7 TB/s of
+// all bytes); 1536 over 377 groups of 4608 x 2304, 368 us (5.8); 8 rows of 8
+// groups, 22 us (4.1: the start and the end weigh).  Loads in operand order
+// took 656 to 670 and 421 to 450, a workgroup per 64 weight rows 628 and 389.
 #include "group_product.h"
 
 namespace moe {
