@@ -10,6 +10,7 @@
 #include "../../include/moe.h"
 #include "launch.h"
 #include "moe_common.h"
+#include "operators.h"
 
 using namespace moe;
 

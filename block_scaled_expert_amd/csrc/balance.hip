@@ -19,8 +19,7 @@
 // so the sums over experts are lane exchanges.  Sums over tokens are taken
 // in a fixed order (registers, then waves, then token chunks); the counts are
 // integers, whose atomics commute.  Every run gives the same bits.
-#include "moe_common.h"
-#include "launch.h"
+#include "operators.h"
 
 namespace moe {
 

@@ -15,6 +15,7 @@
 
 #include "moe_common.h"
 #include "launch.h"
+#include "operators.h"
 #include "quant_row.h"
 
 #include <algorithm>

@@ -19,8 +19,7 @@
 // no arithmetic on scales at all.
 #pragma once
 
-#include "moe_common.h"
-#include "launch.h"
+#include "operators.h"
 
 namespace moe {
 

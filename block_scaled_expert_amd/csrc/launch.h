@@ -19,7 +19,7 @@ struct ActGs {
 };
 
 // Activation quantization of `rows` rows (further limited by *rows_dev when
-// non-null) of width `cols`.  fmt: 1 NVFP4, 2 MXFP8, 4 MXFP4 (ag ignored in both).  dtype: 0
+// non-null) of width `cols`.  fmt: 1 NVFP4, 2 MXFP8 (ag ignored).  dtype: 0
 // bf16, 1 fp32.
 int launch_quant(int fmt, int dtype, const void* x, int rows, const int* rows_dev, int cols,
                  uint8_t* codes, uint8_t* scales, float* gs, hipStream_t stream, const ActGs& ag = ActGs{});
@@ -97,69 +97,12 @@ int launch_route_prep(const RoutePrepArgs& a, int fmt, int gs_mode, hipStream_t 
 // Weight encoding: nmat matrices [rows][cols] (dtype 0 bf16, 1 fp32) to
 // canonical NVFP4 (fmt 1: one fp32 scale per matrix, written to
 // gs[(m / gs_group) * gs_stride + m % gs_group]; amax: nmat words of device
-// scratch), MXFP8 (fmt 2) or MXFP4 (fmt 4), and back to fp32.
+// scratch) or MXFP8 (fmt 2), and back to fp32.
 int launch_encode_weights(int fmt, int dtype, const void* w, int nmat, int rows, int cols, uint8_t* codes,
                           uint8_t* scales, float* gs, int gs_group, int gs_stride, uint32_t* amax,
                           hipStream_t stream);
 int launch_decode_weights(int fmt, const uint8_t* codes, const uint8_t* scales, const float* gs, int nmat, int rows,
                           int cols, int gs_group, int gs_stride, float* out, hipStream_t stream);
-
-// MXFP4 (mxfp4.hip): rows of `cols` elements (a multiple of 32) encoded and
-// decoded, and rows [g | u] of the fp32 gate/up product through the capped
-// SwiGLU to MXFP4 rows of F columns.  rows_dev: device row count that further
-// limits `rows` (nullable for the encoder).
-int launch_mxfp4_encode(int dtype, const void* x, long rows, const int* rows_dev, int cols, uint8_t* codes,
-                        uint8_t* scales, hipStream_t stream);
-int launch_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, long n, float* out, hipStream_t stream);
-int launch_swiglu_mxfp4(const float* gu, int rows, const int* rows_dev, int F, int form, float cap, uint8_t* codes,
-                        uint8_t* scales, hipStream_t stream);
-
-// Grouped MXFP4 product (group_product.hip).
-struct ProductArgs {
-  const uint8_t* a;         // [a_rows][K/2] codes, [a_rows][K/32] scales
-  const uint8_t* a_sc;
-  int a_rows;
-  const int32_t* row_ids;   // nullable: row r reads A row row_ids[r] / id_div
-  int id_div;
-  int M;                    // rows of out
-  int expect;               // rows that the groups are expected to hold, at most M: what the kernel is chosen by
-  const uint8_t* w;         // [G][N][K/2], [G][N][K/32]
-  const uint8_t* w_sc;
-  int G, N, K;
-  const int32_t* offsets;   // [G+1]
-  void* out;                // [M][N]
-  int out_f32;
-};
-int launch_group_product(const ProductArgs& p, hipStream_t stream);
-
-// Router balance loss (balance.hip).  z: dtype 0 bf16, 1 fp32.
-struct BalanceArgs {
-  const void* z;            // [T][E] logits
-  int dtype, T, E, k;
-  const int32_t* ids;       // [T][k]
-  const int32_t* bounds;    // [S+1] first token of each sequence; null: one sequence of T
-  int S;
-  const uint8_t* mask;      // [T] nullable: 0 = not a token
-  int32_t* counts;          // [S][E]
-  int32_t* live;            // [S]
-  // forward
-  float* probs;             // [S][E]
-  float* loss;              // [S]
-  void* ws;
-  // backward
-  const float* d_loss;      // [S]
-  const float* d_w;         // [T][k] nullable
-  int norm_topk;
-  float routed_scale;
-  void* dz;                 // [T][E], z's type
-};
-size_t balance_ws_bytes(int T, int E, int S);
-int launch_balance_forward(const BalanceArgs& a, hipStream_t stream);
-int launch_balance_backward(const BalanceArgs& a, hipStream_t stream);
-
-// The S split-K planes of router logits added in split order, as the top-k
-// adds them: z [T][E].
-int launch_router_logits_sum(const float* zpart, int T, int E, float* z, hipStream_t stream);
 
 struct GemmArgs {
   int fmt;                 // 1 NVFP4, 2 MXFP8

@@ -85,13 +85,6 @@ __host__ __device__ inline int mx_exponent(float amax) {
   return e < -127 ? -127 : e;
 }
 
-// The same for an MXFP4 block (E2M1 elements, emax 2).  An infinite maximum
-// gives exponent 126, so 2^-E is a normal fp32 number.
-__host__ __device__ inline int mxfp4_exponent(float amax) {
-  const int e = (int)((f_bits(amax) >> 23) & 0xFFu) - 127 - 2;
-  return e < -127 ? -127 : e;
-}
-
 // gfx950's conversion instructions (v_cvt_scalef32_pk_fp8_f32,
 // v_cvt_scalef32_pk_fp4_f32, scale 1.0) give the same codes as the encoders
 // above for every finite input: checked on the device over every finite

@@ -14,8 +14,7 @@
 // x 4608 bf16 encoded in 27.3 us (7.0 TB/s), decoded to fp32 in 47.7 (7.2); 8 x
 // 2304 x 4608 fp32 encoded in 70.8 (5.4), decoded in 53.8 (7.2); 64 x 4608 bf16
 // in 2.7 each, a launch's own time.
-#include "moe_common.h"
-#include "launch.h"
+#include "operators.h"
 
 namespace moe {
 

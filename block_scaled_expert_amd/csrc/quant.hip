@@ -5,6 +5,7 @@
 // hits the cache) and every output byte written once.
 #include "quant_row.h"
 #include "launch.h"
+#include "operators.h"
 
 namespace moe {
 
