@@ -113,14 +113,15 @@ __device__ __forceinline__ void store_tile(const ProductArgs& p, const Item& it,
   for (int i = 0; i < NSUB; i++)
 #pragma unroll
     for (int q = 0; q < 16; q++) {
-      const int dm = 32 * i + 8 * (q / 4) + q % 4, so = dm * p.N * kEl;
+      const int dm = 32 * i + 8 * (q / 4) + q % 4;
+      const uint32_t row = (uint32_t)dm * p.N * kEl;   // below 2^29, so an offset from kNowhere stays outside
       bool zero = false;
       if (bad) zero = m0 + dm < it.rows && src[m0 + dm] < 0;
 #pragma unroll
       for (int c = 0; c < C::sn; c++) {
         const float v = zero ? 0.0f : acc[i][c][q];
-        if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b32(f_bits(v), out, (int)at[c], so, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), out, (int)at[c], so, 0);
+        if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b32(f_bits(v), out, (int)(at[c] + row), 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), out, (int)(at[c] + row), 0, 0);
       }
       __builtin_amdgcn_sched_barrier(0);   // one row at a time: the accumulators leave no registers for more
     }

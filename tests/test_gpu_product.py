@@ -207,3 +207,25 @@ def test_mean_group_of_ten(gpu_lib, G, M, N, K, kind, out_f32):
     """Both sides of the streaming kernel's bound, with groups of more and of
     fewer rows than either kernel's tile."""
     test_product(gpu_lib, G, M, N, K, kind, out_f32)
+
+
+@pytest.mark.parametrize("out_f32", [True, False])
+@pytest.mark.parametrize("M,N,K", [(300, 70, 96), (300, 272, 160), (12400, 1003, 32)])
+def test_rows_past_a_partial_tile(gpu_lib, M, N, K, out_f32):
+    """Tiles of 128 rows that hold fewer: the rows after the group's last keep
+    what they held, as do those after the end of out.  Both tile widths."""
+    import torch
+    g = np.random.default_rng(M + N)
+    a, asc = _operand(g, M, K)
+    w, wsc = _operand(g, N, K)
+    ta, tas, tw, tws = to_dev(a), to_dev(asc), to_dev(w[None]), to_dev(wsc[None])
+    for live in (1, 31, 33, 64, 66, 97, 127, 129, M):
+        off = to_dev(np.array([0, live], np.int32))
+        whole = torch.full((M + 160, N), float("nan"), dtype=torch.float32 if out_f32 else torch.bfloat16, device="cuda")
+        gpu_lib.group_product("mxfp4", ta, tas, tw, tws, off, whole[:M])
+        got = whole.float().cpu().numpy()
+        assert np.isnan(got[live:]).all(), live
+        if live <= 300:
+            _check(got, a, asc, w[None], wsc[None], [0, live], out_f32, np.arange(M))
+        else:
+            assert not np.isnan(got[:live]).any()
