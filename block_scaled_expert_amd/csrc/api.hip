@@ -322,6 +322,7 @@ int moe_decode_weights(int32_t fmt, const uint8_t* codes, const uint8_t* scales,
   if ((long)nmat * rows > (1L << 30) || (long)nmat * rows * cols > (1L << 40)) return MOE_ERR_INVALID_ARG;
   if (nmat == 0) return MOE_OK;
   if (codes == nullptr || scales == nullptr || out == nullptr || !aligned(codes, 8)) return MOE_ERR_INVALID_ARG;
+  if (fmt == MOE_FMT_MXFP4 && !aligned(out, 16)) return MOE_ERR_INVALID_ARG;   // written 16 bytes at a time
   if (fmt == MOE_FMT_NVFP4 && (gs == nullptr || gs_group < 1 || gs_stride < gs_group)) return MOE_ERR_INVALID_ARG;
   const int d = device_check();
   if (d != MOE_OK) return d;

@@ -160,3 +160,15 @@ def test_oracle_balance_closed_forms():
         total = float((f["loss"] * d_loss).sum())
         only = B.balance_loss(z, ids, d_loss, E, k, f["counts"], bounds, mask)
         assert abs(total - only) <= 1e-12 * abs(total)
+
+
+def test_decode_arguments(lib):
+    """moe_decode_weights: what its vector accesses need is refused otherwise."""
+    def call(fmt=4, codes=P, scales=P, gs=P, out=P, rows=2, cols=64):
+        return lib.moe_decode_weights(fmt, codes, scales, gs, 1, 1, 1, rows, cols, out, None)
+
+    at = ctypes.c_void_p
+    for kw in (dict(out=at(0x100004)), dict(out=at(0x100008)), dict(codes=at(0x100004)), dict(out=None),
+               dict(codes=None), dict(scales=None), dict(cols=48), dict(rows=0)):
+        assert call(**kw) == -1, kw
+    assert call(fmt=3) == -5
