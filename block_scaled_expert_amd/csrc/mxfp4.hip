@@ -123,7 +123,8 @@ __global__ __launch_bounds__(256) void k_mxfp4_decode(const uint8_t* __restrict_
         const uint32_t c = (w[u] >> (4 * j)) & 15u, m = c & 7u;
         // magnitude from the fields: subnormal 0 / 0.5, else (1 + m/2) 2^(e-1)
         const float mag = m < 2 ? 0.5f * (float)m : bits_f(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-        o[j] = __builtin_amdgcn_ldexpf((c & 8u) ? -mag : mag, e[u]);
+        const float v = __builtin_amdgcn_ldexpf((c & 8u) ? -mag : mag, e[u]);
+        o[j] = e[u] == 128 ? __builtin_nanf("") : v;   // byte 255 is E8M0's NaN, as in the product
       }
       if constexpr (NT) __builtin_nontemporal_store(o, reinterpret_cast<v4f*>(out + i));
       else *reinterpret_cast<v4f*>(out + i) = o;

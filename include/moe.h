@@ -259,8 +259,9 @@ int moe_encode_weights(int32_t fmt, int32_t dtype, const void* w, int32_t nmat, 
  * element = (E2M1 value * E4M3 block scale) * gs (the first product exact,
  * one fp32 rounding), MXFP8 element = E4M3 value * 2^(scale - 127) (one
  * fp32 rounding; may overflow to inf above the fp32 range), MXFP4 element =
- * E2M1 value * 2^(scale - 127) (likewise).  Layouts and gs addressing as in
- * moe_encode_weights; codes 8-byte aligned, for MXFP4 out 16. */
+ * E2M1 value * 2^(scale - 127) (likewise; a scale byte of 255, E8M0's NaN,
+ * which the encoder never writes, makes its block NaN).  Layouts and gs
+ * addressing as in moe_encode_weights; codes 8-byte aligned, for MXFP4 out 16. */
 int moe_decode_weights(int32_t fmt, const uint8_t* codes, const uint8_t* scales, const float* gs,
                        int32_t gs_group, int32_t gs_stride, int32_t nmat, int32_t rows, int32_t cols, float* out,
                        void* stream);

@@ -214,11 +214,13 @@ def quantize_mxfp4(v: np.ndarray):
 
 
 def dequantize_mxfp4(packed, scales) -> np.ndarray:
-    """MXFP4 -> float64 values (exact)."""
+    """MXFP4 -> float64 values (exact); a scale byte of 255, E8M0's NaN, makes
+    its block NaN."""
     codes = unpack_nibbles(np.asarray(packed, dtype=np.uint8))
     K = codes.shape[-1]
     vals = e2m1_decode(codes).reshape(codes.shape[:-1] + (K // MX_BLOCK, MX_BLOCK))
-    return (vals * e8m0_decode(scales)[..., None]).reshape(codes.shape)
+    step = np.where(np.asarray(scales) == 255, np.nan, e8m0_decode(scales))
+    return (vals * step[..., None]).reshape(codes.shape)
 
 
 # --------------------------------------------------------------------------

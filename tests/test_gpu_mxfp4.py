@@ -149,3 +149,18 @@ def test_route_logits_are_the_routers(gpu_lib):
         s = 1.0 / (1.0 + np.exp(-z.cpu().numpy().astype(np.float64)))
         got = np.take_along_axis(s, ids.cpu().numpy().astype(np.int64), 1)
         assert np.abs(got - tw.cpu().numpy()).max() <= 4e-7      # expf and the division, a few ulp of a score below 1
+
+
+def test_decode_every_scale(gpu_lib):
+    """Every code under every scale byte: 2^127 still decodes, 255 (E8M0's NaN)
+    makes its whole block NaN, as it does in the product."""
+    import torch
+    codes = np.tile(np.arange(256, dtype=np.uint8), (1, 256, 1))          # 16 blocks a row: every byte
+    sc = np.repeat(np.arange(256, dtype=np.uint8).reshape(1, 256, 1), 16, axis=2)
+    out = torch.empty((1, 256, 512), dtype=torch.float32, device="cuda")
+    gpu_lib.decode_weights("mxfp4", to_dev(codes), to_dev(sc), out)
+    with np.errstate(over="ignore"):
+        ref = F.dequantize_mxfp4(codes, sc).astype(np.float32)
+    got = out.cpu().numpy()
+    assert np.isnan(got[0, 255]).all() and not np.isnan(got[0, :255]).any()
+    assert np.array_equal(got, ref, equal_nan=True)

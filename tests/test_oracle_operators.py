@@ -104,3 +104,11 @@ def test_balance_is_one_when_even():
     z = np.zeros((16, E))
     ids = (np.arange(32).reshape(16, 2) % E).astype(np.int32)
     assert B.balance_forward(z, ids, E, k)["loss"][0] == pytest.approx(1.0, abs=1e-15)
+
+
+def test_mxfp4_scale_255_is_nan():
+    """E8M0 has no value 2^128: byte 255 is its NaN, for every code of the block."""
+    codes = np.resize(np.arange(256, dtype=np.uint8), (3, 16))
+    got = F.dequantize_mxfp4(codes, np.array([[254], [255], [0]], np.uint8))
+    assert np.isnan(got[1]).all() and np.isfinite(got[[0, 2]]).all()
+    assert np.abs(got[0]).max() == 6.0 * 2.0 ** 127
