@@ -77,3 +77,23 @@ def test_balance(gpu_lib):
     want, size = B.balance_backward(zt, it, ref, np.array([3.0]), E, k)
     got = dz[T - n:].float().cpu().numpy()
     assert (np.abs(got - want) <= 4e-6 * size + 2.0 ** -8 * np.abs(want) + 1e-37).all()
+
+
+def test_balance_of_a_long_sequence(gpu_lib):
+    """Equal logits give 1/E however many tokens there are, though the rounding
+    errors of equal terms do not average out.  Bound: a probability 2e-6; runs
+    of at most 256 additions, joined over 32 runs, 4 waves, 32 slots of one
+    lane group and 4 + 16 partial sums, each within 2^-24."""
+    import torch
+    T, E = 1 << 26, 5
+    cfg = gpu_lib.Config(num_experts=E, top_k=1)
+    z = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    ids = (torch.arange(T, dtype=torch.int32, device="cuda") % E).reshape(T, 1)
+    counts, live = torch.empty((1, E), dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    probs, loss = torch.empty((1, E), device="cuda"), torch.empty(1, device="cuda")
+    gpu_lib.balance_forward(cfg, z, ids, counts, live, probs, loss, gpu_lib.balance_workspace(cfg, T))
+    assert live.cpu().tolist() == [T]
+    assert counts[0].cpu().tolist() == [(T - e + E - 1) // E for e in range(E)]
+    tol = 2e-6 + (256 + 32 + 4 + 32 + 20) * 2.0 ** -24
+    assert (probs[0].double() * E - 1).abs().max().item() <= tol
+    assert abs(loss[0].item() - 1) <= tol + 2e-6
