@@ -67,13 +67,10 @@ __device__ inline uint32_t encode8(float (&v)[8], int& E) {
 
 constexpr int kEncUnroll = 2;   // loads in flight per lane (16384 x 4608 bf16 to codes and back: 81 us; 4: 85, 8: 91)
 
-// n elements (a multiple of 32), 8 per lane and pass.  rows_dev (nullable):
-// device row count that further limits the rows of `cols` elements.
+// n elements (a multiple of 32), 8 per lane and pass.
 template <typename InT, bool NT>
-__global__ __launch_bounds__(256) void k_mxfp4_encode(const InT* __restrict__ x, long n,
-                                                      const int* __restrict__ rows_dev, int cols,
-                                                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  if (rows_dev != nullptr) n = min(n, (long)max(*rows_dev, 0) * cols);
+__global__ __launch_bounds__(256) void k_mxfp4_encode(const InT* __restrict__ x, long n, uint8_t* __restrict__ codes,
+                                                      uint8_t* __restrict__ scales) {
   constexpr long kPass = 256 * 8 * kEncUnroll;
   for (long base = blockIdx.x * kPass + 8 * threadIdx.x; base < n; base += gridDim.x * kPass) {
     float v[kEncUnroll][8];
@@ -157,15 +154,12 @@ static unsigned pass_grid(long n, long per) {
   return (unsigned)(g < (1L << 20) ? g : (1L << 20));
 }
 
-int launch_mxfp4_encode(int dtype, const void* x, long rows, const int* rows_dev, int cols, uint8_t* codes,
-                        uint8_t* scales, hipStream_t stream) {
-  const long n = rows * cols;
+int launch_mxfp4_encode(int dtype, const void* x, long n, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
   if (n <= 0) return 0;
   const dim3 grid(pass_grid(n, 2048L * kEncUnroll));
   const bool nt = (size_t)n * (dtype == 0 ? 2 : 4) > kStreamBytes;
-#define MOE_ENC(T, NT)                                                                                            \
-  hipLaunchKernelGGL((k_mxfp4_encode<T, NT>), grid, dim3(256), 0, stream, (const T*)x, n, rows_dev, cols, codes, \
-                     scales)
+#define MOE_ENC(T, NT) \
+  hipLaunchKernelGGL((k_mxfp4_encode<T, NT>), grid, dim3(256), 0, stream, (const T*)x, n, codes, scales)
   if (dtype == 0) {
     if (nt) MOE_ENC(uint16_t, true);
     else MOE_ENC(uint16_t, false);

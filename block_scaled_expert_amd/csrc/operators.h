@@ -16,12 +16,12 @@ __host__ __device__ inline int mxfp4_exponent(float amax) {
   return e < -127 ? -127 : e;
 }
 
-// MXFP4 (mxfp4.hip): rows of `cols` elements (a multiple of 32) encoded and
-// decoded, and rows [g | u] of the fp32 gate/up product through the capped
-// SwiGLU to MXFP4 rows of F columns.  rows_dev: device row count that further
-// limits `rows` (nullable for the encoder).
-int launch_mxfp4_encode(int dtype, const void* x, long rows, const int* rows_dev, int cols, uint8_t* codes,
-                        uint8_t* scales, hipStream_t stream);
+// MXFP4 (mxfp4.hip): n elements (a multiple of 32) encoded and decoded, and
+// rows [g | u] of the fp32 gate/up product through the capped SwiGLU to MXFP4
+// rows of F columns.  rows_dev: device row count that further limits `rows`.
+// launch_quant takes none with this format: the layer's h, whose row count is
+// on the device, is encoded by launch_swiglu_mxfp4.
+int launch_mxfp4_encode(int dtype, const void* x, long n, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 int launch_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, long n, float* out, hipStream_t stream);
 int launch_swiglu_mxfp4(const float* gu, int rows, const int* rows_dev, int F, int form, float cap, uint8_t* codes,
                         uint8_t* scales, hipStream_t stream);

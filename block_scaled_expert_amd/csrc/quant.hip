@@ -94,7 +94,7 @@ int launch_act_gs_tensor(int dtype, const void* x, int rows, const int* rows_dev
 int launch_quant(int fmt, int dtype, const void* x, int rows, const int* rows_dev, int cols,
                  uint8_t* codes, uint8_t* scales, float* gs, hipStream_t stream, const ActGs& ag) {
   if (rows <= 0) return 0;
-  if (fmt == 4) return launch_mxfp4_encode(dtype, x, rows, rows_dev, cols, codes, scales, stream);
+  if (fmt == 4) return rows_dev != nullptr ? -1 : launch_mxfp4_encode(dtype, x, (long)rows * cols, codes, scales, stream);
   const dim3 grid(rows), block(256);
   if (fmt == 1) {
 #define MOE_QNV(T, M)                                                                                            \
