@@ -127,14 +127,14 @@ struct Item {
   int g, row0, rows, bx;
 };
 constexpr int kPanelTiles = 8;
-// `offset(i)`: the i-th of G + 1 offsets, clamped to [0, M]; hw: the
-// workgroup's number, or where one works through several, its next one.
-template <int TM, int PER, typename F>
-__device__ inline bool find_item_n(F offset, int G, int nx, int hw, Item& it) {
+__device__ inline int clamped_offset(const ProductArgs& p, int i) { return min(max(p.offsets[i], 0), p.M); }
+// hw: the workgroup's number.
+template <int TM, int PER>
+__device__ inline bool find_item_n(const ProductArgs& p, int nx, int hw, Item& it) {
   const int lane = threadIdx.x & 63, g0 = PER * lane;
   int at[PER + 1], n = 0;
 #pragma unroll
-  for (int i = 0; i <= PER; i++) at[i] = offset(min(g0 + i, G));
+  for (int i = 0; i <= PER; i++) at[i] = clamped_offset(p, min(g0 + i, p.G));
 #pragma unroll
   for (int i = 0; i < PER; i++) n += (max(at[i + 1] - at[i], 0) + TM - 1) / TM;
   int end = n;                                  // inclusive scan over the lanes
@@ -171,13 +171,12 @@ __device__ inline bool find_item_n(F offset, int G, int nx, int hw, Item& it) {
   it.rows = min(TM, len - tile * TM);
   return true;
 }
-template <int TM, typename F>
-__device__ inline bool find_item(F offset, int G, int nx, int hw, Item& it) {
-  if (G <= 64) return find_item_n<TM, 1>(offset, G, nx, hw, it);
-  if (G <= 512) return find_item_n<TM, 8>(offset, G, nx, hw, it);
-  return find_item_n<TM, 16>(offset, G, nx, hw, it);
+template <int TM>
+__device__ inline bool find_item(const ProductArgs& p, int nx, int hw, Item& it) {
+  if (p.G <= 64) return find_item_n<TM, 1>(p, nx, hw, it);
+  if (p.G <= 512) return find_item_n<TM, 8>(p, nx, hw, it);
+  return find_item_n<TM, 16>(p, nx, hw, it);
 }
-__device__ inline int clamped_offset(const ProductArgs& p, int i) { return min(max(p.offsets[i], 0), p.M); }
 // Upper bound of the tiles of a call.
 inline int max_tiles(const ProductArgs& p, int tm) {
   const long n = p.G + (long)p.M / tm;

@@ -34,8 +34,7 @@ __global__ __launch_bounds__(256, 4) void k_product_stream(ProductArgs p, int pa
   int* const src = reinterpret_cast<int*>(ls + (size_t)panel * 64);                // [kStreamRows]
 
   Item it;
-  if (!find_item<kStreamRows>([&](int i) { return clamped_offset(p, i); }, p.G, (p.N + 64 * NT - 1) / (64 * NT), blockIdx.x, it))
-    return;
+  if (!find_item<kStreamRows>(p, (p.N + 64 * NT - 1) / (64 * NT), blockIdx.x, it)) return;
   const int g = it.g, m0 = it.row0, rows = it.rows, n0 = it.bx * 64 * NT;
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;

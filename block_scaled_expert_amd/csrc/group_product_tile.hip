@@ -269,8 +269,7 @@ __global__ __launch_bounds__(64 * MW * NW, SM * SN > 4 ? 2 : 4) void k_product_t
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   int* const src = reinterpret_cast<int*>(lds + C::kLds);                    // [BM]
   Item it;
-  if (!find_item<C::BM>([&](int i) { return clamped_offset(p, i); }, p.G, (p.N + C::BN - 1) / C::BN, blockIdx.x, it))
-    return;
+  if (!find_item<C::BM>(p, (p.N + C::BN - 1) / C::BN, blockIdx.x, it)) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (tid < C::BM) src[tid] = tid < it.rows ? source_row(p, it.row0 + tid) : -1;
   __syncthreads();
