@@ -14,7 +14,9 @@
 // The forward reads the logits once and the backward once: HBM-bound at
 // large T, launch-bound below.  Measured, 131072 x 384 fp32 and 8 ids a token:
 // forward 47 us + 10 for its second launch (4.4 TB/s), backward 76 (5.4 TB/s);
-// 16384 tokens 8.6 + 7.2 and 15.6; 64 tokens 6.3 in one launch and 4.4.  One
+// 16384 tokens 8.6 + 7.2 and 15.6; 64 tokens 6.3 in one launch and 4.4.  bf16
+// logits take nearly fp32's time (44 + 10 and 73 at 131072 tokens): half the
+// bytes, but as many loads and stores and the same arithmetic an element.  One
 // wavefront holds a token's whole row in registers (lane l experts l + 64 i),
 // so the sums over experts are lane exchanges.  Sums over tokens are taken
 // in a fixed order (registers, then waves, then token chunks); the counts are

@@ -4,11 +4,15 @@
 //   out[r][n] = sum_k A[src(r)][k] W[g(r)][n][k]
 //
 // for rows r in [offsets[g], offsets[g+1]).  Both operands are E2M1 codes
-// with an E8M0 scale per 32 of k; v_mfma_scale_f32_16x16x128_f8f6f4 takes the
-// codes and the scales as they are stored and accumulates in fp32, so no
-// operand is expanded.  Operand layout (checked on the device by the parity
-// tests): lane l holds row l % 16 and one block of 32 k (16 bytes) in lane
-// group l / 16, and one byte of its scale register applies to that block.
+// with an E8M0 scale per 32 of k; the scaled f8f6f4 instructions take the codes
+// and the scales as they are stored and accumulate in fp32, so no operand is
+// expanded.  What both kernels share is how the work is handed out (Item) and
+// the views of memory; the tile kernel's instruction is in its own file.
+//
+// The streaming kernel uses v_mfma_scale_f32_16x16x128_f8f6f4.  Operand layout
+// (checked on the device by the parity tests): lane l holds row l % 16 and one
+// block of 32 k (16 bytes) in lane group l / 16, and one byte of its scale
+// register applies to that block.
 // Accumulator register q of lane l is out[4 (l / 16) + q][l % 16].
 //
 // The sum over k does not care which blocks meet in one instruction as long

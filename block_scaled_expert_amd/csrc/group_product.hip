@@ -156,7 +156,9 @@ static void launch_stream(const ProductArgs& p, hipStream_t stream) {
 // sizes): 384 groups of 4608 x 4608 458/522, 745/828, 814/865, 932/886,
 // 1215/911, 1284/952; 48 of them 65/88, 101/121, 107/123, 127/123, 165/124,
 // 205/130; 384 of 4608 x 2304 214/286, 358/449, 409/461, 458/466, 599/476,
-// 642/505.
+// 642/505.  The mean counts empty groups, so rows that crowd into a few of many
+// groups stream all the same: 8 of 384 groups with 480, 64 and 32 rows each (4608
+// x 4608, fp32 out) 412/70, 80/27 and 57/22; 121 of them with 30 rows each 533/310.
 int launch_group_product(const ProductArgs& p, hipStream_t stream) {
   if (p.M <= 0) return 0;
   if ((long)p.expect > 10L * p.G) return launch_product_tile(p, stream);

@@ -11,16 +11,16 @@
 // 64-byte piece.  So the loads take a half step (k 128, 64 bytes) of 16 rows per
 // wave, row after row, and LDS does the rearrangement.
 //
-// Pipeline, in half steps h: h + 2 is loaded straight to LDS (3 slots) while h
-// is multiplied; one barrier a half step, passed with the youngest half step's
-// loads still on their way.  Scales: 16 bytes (4 half steps, a pass) of a row
+// Pipeline, in half steps h: after h's products the loads of h + 2 go out,
+// straight to LDS (3 slots), and arrive while h + 1 is multiplied; one barrier a
+// half step, passed with the youngest half step's loads still on their way.  Scales: 16 bytes (4 half steps, a pass) of a row
 // per load, through registers, turned so that a lane's 8 bytes are two words
 // whose bytes the instructions select.  The large tile is 4 waves of 128 x 64
 // (199 registers, 78 KiB of LDS), so that two workgroups share a CU and one
 // multiplies while the other starts, ends or waits.
 //
-// Measured (48 groups, 16384 rows x 4608 x 4608, bf16 out): 292 us, 2.4
-// PFLOP/s; with the operands going to LDS through registers 307; 256 x 256
+// Measured (48 groups, 16384 rows x 4608 x 4608): bf16 out 292 us, 2.4
+// PFLOP/s; fp32 out, what the layer's gate/up takes, 309; bf16 with the operands going to LDS through registers 307; 256 x 256
 // tiles of 8 waves 293, 128 x 128 of 4 335; with the weights brought to operand
 // order in registers instead of through LDS 310.  No unit is near its rate.
 // Without the loads it takes 184, with loads that all hit a cache 251, without
@@ -234,7 +234,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, const Item& i
   loads_barrier<C::PA + C::PW>();
   int slot = 0, free_slot = 2 * C::kSlot;                // of half steps h and h + 2
   auto next_slot = [&](int s) { return s == 2 * C::kSlot ? 0 : s + C::kSlot; };
-  // 4 half steps per pass: scale bytes by h % 4, register set h % 2
+  // 4 half steps per pass: scale bytes by h % 4
   for (int h0 = 0; h0 < halves; h0 += 4) {
     if constexpr (NSUB > 0) {
 #pragma unroll

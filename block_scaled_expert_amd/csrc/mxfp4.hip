@@ -130,7 +130,11 @@ __global__ __launch_bounds__(256) void k_mxfp4_decode(const uint8_t* __restrict_
 }
 
 // h = capped SwiGLU of rows [g | u] (fp32, 2F wide, the gate/up product),
-// encoded: 8 columns per lane, 4 lanes per block.  Row count on the device.
+// encoded: 8 columns per lane, 4 lanes per block.  Row count on the device, so
+// the grid covers every pair of the call.  Measured: about 16384 local rows of
+// F 2304 (of 131072 pairs) 105 us, 3.1 TB/s, where 322 MB take 62 at a copy's
+// rate: seven of eight workgroups only leave, and the second of a row has 32 of
+// 256 lanes at work.  512 rows 5 us.
 __global__ __launch_bounds__(256) void k_swiglu_mxfp4(const float* __restrict__ gu, const int* __restrict__ rows_dev,
                                                       int F, int form, float cap, float inv_c,
                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {

@@ -307,8 +307,8 @@ int moe_route_logits(const moe_config* cfg, int32_t T, const void* ws, size_t ws
  *  ws: moe_balance_workspace_size bytes of device scratch, 256-byte aligned,
  *  no initial contents needed.  Of cfg only num_experts (at most 1024) and
  *  top_k (at most 32) are read.  T at most 2^26, T top_k at most 2^30,
- *  1 <= S <= 65535.  Two
- *  launches; the same inputs give the same bits. */
+ *  1 <= S <= 65535.  One launch for few tokens (T at most 128 and T
+ *  ceil(E / 64) at most 384), two above; the same inputs give the same bits. */
 int moe_balance_workspace_size(const moe_config* cfg, int32_t T, int32_t S, size_t* bytes);
 int moe_balance_forward(const moe_config* cfg, int32_t dtype, const void* z, int32_t T, const int32_t* topk_ids,
                         const int32_t* seq_offsets, int32_t S, const uint8_t* token_mask, int32_t* counts,
