@@ -6,8 +6,9 @@ ABI in include/moe.h (moe_route, moe_dispatch, moe_quantize_act,
 moe_forward, moe_forward_fused, moe_forward_fused_status, moe_route_forward,
 moe_forward_noalloc, moe_cap_swiglu, moe_workspace_size,
 moe_noalloc_scratch_bytes, moe_check_arch, moe_status_string, the weight
-encoder and decoder, moe_group_product, moe_route_logits, and the router's
-balance loss with its gradient).
+encoder and decoder, moe_group_product, moe_group_matvec, moe_route_logits,
+the router's balance loss with its gradient, the residual norm with its
+gradient, moe_forward_quantized, and the sorted rows with their gradients).
 Tensors must be contiguous and on the current CUDA (HIP) device; apart from
 moe_forward_noalloc's fixed device array the library never allocates, so
 callers pass outputs and a workspace.
@@ -37,7 +38,9 @@ EXPORTED = ("moe_status_string", "moe_check_arch", "moe_validate_config", "moe_w
             "moe_forward_fused", "moe_forward_fused_status", "moe_cap_swiglu", "moe_encode_weights",
             "moe_decode_weights", "moe_forward_noalloc", "moe_noalloc_scratch_bytes", "moe_route_forward",
             "moe_route_logits", "moe_balance_workspace_size", "moe_balance_forward", "moe_balance_backward",
-            "moe_group_product")
+            "moe_group_product", "moe_group_matvec", "moe_norm_forward", "moe_norm_workspace_size",
+            "moe_norm_backward", "moe_forward_quantized", "moe_sort_rows", "moe_sort_rows_backward",
+            "moe_combine_rows", "moe_combine_rows_backward")
 LAYOUT_CANONICAL, LAYOUT_PACKED = 0, 1
 
 
@@ -100,6 +103,18 @@ def load() -> ctypes.CDLL:
     lib.moe_balance_backward.argtypes = [ctypes.POINTER(CConfig), i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                          vp]
     lib.moe_group_product.argtypes = [i32, vp, vp, i32, vp, i32, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+    lib.moe_group_matvec.argtypes = [ctypes.POINTER(CConfig), i32, i32, vp, i32, vp, i32, i32, vp, vp, vp, i32, i32, i32,
+                                     i32, i32, vp, i32, vp, vp]
+    lib.moe_norm_forward.argtypes = [ctypes.POINTER(CConfig), i32, vp, i32, vp, i32, i32, vp, ctypes.c_float, vp, vp, vp,
+                                     vp, vp, vp, vp]
+    lib.moe_norm_workspace_size.argtypes = [i32, i32, ctypes.POINTER(sz)]
+    lib.moe_norm_backward.argtypes = [i32, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_forward_quantized.argtypes = [ctypes.POINTER(CConfig), vp, vp, vp, i32, vp, vp, ctypes.POINTER(CWeights), vp,
+                                          vp, sz, vp, vp]
+    lib.moe_sort_rows.argtypes = [i32, vp, i32, i32, i32, vp, i32, vp, vp]
+    lib.moe_sort_rows_backward.argtypes = [i32, vp, i32, vp, i32, i32, i32, vp, vp]
+    lib.moe_combine_rows.argtypes = [i32, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.moe_combine_rows_backward.argtypes = [i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp]
     for name in EXPORTED:
         if name != "moe_status_string":
             getattr(lib, name).restype = ctypes.c_int
@@ -399,6 +414,165 @@ def group_product(fmt: str, a, a_scales, w, w_scales, offsets, out, row_ids=None
                                  _stream()), "moe_group_product")
 
 
+def _dtype(t, name: str) -> int:
+    """MOE_DTYPE of a bf16 or fp32 tensor."""
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise ValueError(f"{name} must be bfloat16 or float32")
+
+
+def group_matvec(fmt: str, x, w, w_scales, offsets, out, gs=None, gs_group: int = 1, gs_stride: int = 1, row_ids=None,
+                 id_div: int = 1, swiglu: Config | None = None) -> None:
+    """out[r] = x[src(r)] @ W[g].T for rows r in [offsets[g], offsets[g+1]),
+    src(r) = r, or row_ids[r] // id_div; x bf16 or fp32 [rows, K], W 4-bit.
+    w / w_scales: uint8 codes [G, N, K/2] and scales [G, N, K/16] (fmt
+    "nvfp4") or [G, N, K/32] ("mxfp4"); NVFP4: gs, gs_group and gs_stride as in
+    encode_weights; offsets int32 [G+1]; out [M, N] fp32 or bf16; row_ids int32
+    [M].  swiglu: a Config whose capped SwiGLU is taken over [gate | up], out is
+    then [M, N/2]."""
+    import torch
+    if fmt not in FMTS:
+        raise ValueError(f"unknown format {fmt!r}")
+    rows, K = x.shape
+    G, N = w.shape[:2]
+    M = out.shape[0]
+    nv = fmt == "nvfp4"
+    if nv:
+        if gs_group < 1 or N % gs_group:
+            raise ValueError("N must be a multiple of gs_group")
+        _check_gs(gs, G * gs_group, gs_group, gs_stride)
+    cc = None if swiglu is None else ctypes.byref(swiglu.c())
+    _ok(load().moe_group_matvec(cc, FMTS[fmt], _dtype(x, "x"), _ptr(x, None, None, "x"), rows,
+                                _ptr(row_ids, torch.int32, (M,), "row_ids"), id_div, M,
+                                _ptr(w, torch.uint8, (G, N, _code_cols(fmt, K)), "w"),
+                                _ptr(w_scales, torch.uint8, (G, N, _scale_cols(fmt, K)), "w_scales"),
+                                _ptr(gs, torch.float32, None, "gs") if nv else None, gs_group, gs_stride, G, N, K,
+                                _ptr(offsets, torch.int32, (G + 1,), "offsets"), _dtype(out, "out"),
+                                _ptr(out, None, (M, N if swiglu is None else N // 2), "out"), _stream()),
+        "moe_group_matvec")
+
+
+def norm_forward(x, weight, y=None, residual=None, res_out=None, rstd=None, eps: float = 1e-6, cfg=None, codes=None,
+                 scales=None, row_gs=None) -> None:
+    """res_out = x + residual; y = res_out * rstd * weight, rstd = (mean of
+    res_out^2 + eps)^-1/2 per row; and the codes of y in cfg's format (a Config,
+    or a format name for the per-row default) as quantize_act writes them.
+    x, y [T, cols] bf16 or fp32; residual, res_out [T, cols] of x's type or
+    fp32; weight [cols] and rstd [T] fp32.  Without cfg no codes are written."""
+    import torch
+    if isinstance(cfg, str):
+        cfg, cc = _default_config(cfg)
+    else:
+        cc = None if cfg is None else cfg.c()
+    T, cols = x.shape
+    res = residual if residual is not None else res_out
+    res_type = None if res is None else res.dtype
+    enc = (None, None, None)
+    if cfg is not None:
+        enc = (_ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, cols)), "codes"),
+               _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, cols)), "scales"),
+               _ptr(row_gs, torch.float32, (T,), "row_gs") if cfg.fmt == "nvfp4" else None)
+    elif codes is not None or scales is not None or row_gs is not None:
+        raise ValueError("codes, scales and row_gs need cfg")
+    _ok(load().moe_norm_forward(None if cc is None else ctypes.byref(cc), _dtype(x, "x"), _ptr(x, None, None, "x"),
+                                _dtype(x if res is None else res, "residual"),
+                                _ptr(residual, res_type, (T, cols), "residual"), T, cols,
+                                _ptr(weight, torch.float32, (cols,), "weight"), eps,
+                                _ptr(res_out, res_type, (T, cols), "res_out"), _ptr(y, x.dtype, (T, cols), "y"),
+                                _ptr(rstd, torch.float32, (T,), "rstd"), *enc, _stream()), "moe_norm_forward")
+
+
+def norm_workspace_size(T: int, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    _ok(load().moe_norm_workspace_size(T, cols, ctypes.byref(n)), "moe_norm_workspace_size")
+    return n.value
+
+
+def norm_workspace(T: int, cols: int, device="cuda"):
+    import torch
+    return torch.empty(norm_workspace_size(T, cols), dtype=torch.uint8, device=device)
+
+
+def norm_backward(dy, res, weight, rstd, d_res, ws=None, d_res_out=None, dx=None, d_weight=None) -> None:
+    """d_res [T, cols] (res's type) <- the gradient of the stream res that
+    norm_forward normed (its res_out, or x without a residual), with d_res_out
+    added: the gradient of the residual and of x.  dx: the same in dy's type.
+    d_weight [cols] fp32 needs ws: norm_workspace(T, cols)."""
+    import torch
+    T, cols = dy.shape
+    _ok(load().moe_norm_backward(_dtype(dy, "dy"), _ptr(dy, None, None, "dy"), _dtype(res, "res"),
+                                 _ptr(res, None, (T, cols), "res"), _ptr(d_res_out, res.dtype, (T, cols), "d_res_out"),
+                                 T, cols, _ptr(weight, torch.float32, (cols,), "weight"),
+                                 _ptr(rstd, torch.float32, (T,), "rstd"), _ptr(d_res, res.dtype, (T, cols), "d_res"),
+                                 _ptr(dx, dy.dtype, (T, cols), "dx"),
+                                 _ptr(d_weight, torch.float32, (cols,), "d_weight"),
+                                 _ptr(ws, torch.uint8, None, "ws"), 0 if ws is None else ws.numel(), _stream()),
+        "moe_norm_backward")
+
+
+def _slots(pair_pos, T: int) -> int:
+    """Slots of a token in pair_pos ([T, top_k] or flat)."""
+    n = pair_pos.numel()
+    if pair_pos.dim() == 2 and pair_pos.shape[0] != T or T > 0 and (n == 0 or n % T):
+        raise ValueError(f"pair_pos must hold top_k positions for each of {T} tokens")
+    return n // T if T > 0 else 1
+
+
+def sort_rows(x, pair_pos, out) -> None:
+    """out[pair_pos[t, j]] = x[t] for the local pairs (pair_pos: dispatch's,
+    int32 [T * top_k]).  x [T, cols] and out [M, cols] of one type, bf16 or fp32."""
+    import torch
+    T, cols = x.shape
+    M = out.shape[0]
+    _ok(load().moe_sort_rows(_dtype(x, "x"), _ptr(x, None, None, "x"), T, _slots(pair_pos, T), cols,
+                             _ptr(pair_pos, torch.int32, None, "pair_pos"), M, _ptr(out, x.dtype, (M, cols), "out"),
+                             _stream()), "moe_sort_rows")
+
+
+def sort_rows_backward(d_out, pair_pos, dx) -> None:
+    """dx[t] = sum over the local pairs of d_out[pair_pos[t, j]]: sort_rows' gradient."""
+    import torch
+    T, cols = dx.shape
+    M = d_out.shape[0]
+    _ok(load().moe_sort_rows_backward(_dtype(dx, "dx"), _ptr(d_out, dx.dtype, (M, cols), "d_out"), M,
+                                      _ptr(pair_pos, torch.int32, None, "pair_pos"), T, _slots(pair_pos, T), cols,
+                                      _ptr(dx, None, None, "dx"), _stream()), "moe_sort_rows_backward")
+
+
+def combine_rows(y, pair_pos, topk_w, out) -> None:
+    """out[t] = sum over the local pairs of topk_w[t, j] * y[pair_pos[t, j]]
+    (topk_w fp32 [T, top_k]; None: all 1).  y [M, cols], out [T, cols], each
+    bf16 or fp32."""
+    import torch
+    T, cols = out.shape
+    M, k = y.shape[0], _slots(pair_pos, T)
+    _ok(load().moe_combine_rows(_dtype(y, "y"), _ptr(y, None, (M, cols), "y"), M,
+                                _ptr(pair_pos, torch.int32, None, "pair_pos"),
+                                _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols, _dtype(out, "out"),
+                                _ptr(out, None, None, "out"), _stream()), "moe_combine_rows")
+
+
+def combine_rows_backward(d_out, y, pair_pos, topk_w, dy, d_topk_w=None) -> None:
+    """combine_rows' gradients: dy [M, cols] (y's type; may be y) and d_topk_w
+    [T, top_k] fp32, either of them None.  y may be None where d_topk_w is."""
+    import torch
+    T, cols = d_out.shape
+    k = _slots(pair_pos, T)
+    rows = y if y is not None else dy
+    if rows is None:
+        raise ValueError("dy or y must be given")
+    M = rows.shape[0]
+    _ok(load().moe_combine_rows_backward(_dtype(d_out, "d_out"), _ptr(d_out, None, None, "d_out"), _dtype(rows, "y"),
+                                         _ptr(y, None, (M, cols), "y"), M, _ptr(pair_pos, torch.int32, None, "pair_pos"),
+                                         _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols,
+                                         _ptr(dy, rows.dtype, (M, cols), "dy"),
+                                         _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream()),
+        "moe_combine_rows_backward")
+
+
 def dispatch(cfg: Config, topk_ids, expert_offsets, sorted_pairs=None, pair_pos=None, ws=None) -> None:
     import torch
     T = topk_ids.shape[0]
@@ -462,6 +636,28 @@ def forward(cfg: Config, x, topk_ids, topk_w, weights, out, ws, events=None, fus
            _ptr(topk_w, torch.float32, (T, k), "topk_w"), ctypes.byref(cw),
            _ptr(out, torch.bfloat16, (T, H), "out"), _ptr(ws, torch.uint8, None, "ws"),
            ws.numel(), _stream(), ev), "moe_forward_fused" if fused else "moe_forward")
+
+
+def forward_quantized(cfg: Config, codes, scales, topk_ids, topk_w, weights, out, ws, row_gs=None, events=None) -> None:
+    """forward on tokens quantized already (norm_forward with cfg, or
+    quantize_act at site 0): codes, scales and, for NVFP4, row_gs."""
+    import torch
+    T = codes.shape[0]
+    H, k = cfg.hidden, cfg.top_k
+    cw = weights if isinstance(weights, CWeights) else weights_struct(cfg, weights)
+    ev = None
+    if events is not None:
+        if len(events) != 2 * len(STAGES):
+            raise ValueError("events must hold 2 per stage")
+        ev = (ctypes.c_void_p * len(events))(*[e.cuda_event if e is not None else None for e in events])
+    cc = cfg.c()
+    _ok(load().moe_forward_quantized(ctypes.byref(cc), _ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, H)), "codes"),
+                                     _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, H)), "scales"),
+                                     _ptr(row_gs, torch.float32, (T,), "row_gs") if cfg.fmt == "nvfp4" else None, T,
+                                     _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
+                                     _ptr(topk_w, torch.float32, (T, k), "topk_w"), ctypes.byref(cw),
+                                     _ptr(out, torch.bfloat16, (T, H), "out"), _ptr(ws, torch.uint8, None, "ws"),
+                                     ws.numel(), _stream(), ev), "moe_forward_quantized")
 
 
 def forward_noalloc(cfg: Config, x, topk_ids, topk_w, weights, out) -> None:

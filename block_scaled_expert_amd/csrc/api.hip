@@ -189,6 +189,44 @@ int check_balance(const moe_config* c, int T, int S) {
   return MOE_OK;
 }
 
+// Token rows of the norm and of the sort: one workgroup a row, up to 1024
+// threads, within a launch's 2^32 threads.
+constexpr int kMaxTokenRows = 1 << 21;
+bool known_dtype(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F32; }
+uintptr_t element(int dtype) { return dtype == MOE_DTYPE_BF16 ? 2 : 4; }
+
+int check_norm(int dtype, int res_dtype, int T, int cols) {
+  if (!known_dtype(dtype) || !known_dtype(res_dtype)) return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_DTYPE_F32 && res_dtype == MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxTokenRows || cols < 1 || cols > (1 << 16)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int check_rows(int T, int k, int cols, int M, const int32_t* pos) {
+  if (T < 0 || T > kMaxTokenRows || k < 1 || k > 32 || cols < 1 || cols > (1 << 16)) return MOE_ERR_INVALID_ARG;
+  if (M < 0 || M > (1 << 26)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (pos == nullptr || !aligned(pos, 4))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+RowsArgs rows_args(int T, int k, int cols, int M, const int32_t* pos, const float* w) {
+  RowsArgs a{};
+  a.T = T;
+  a.k = k;
+  a.cols = cols;
+  a.M = M;
+  a.pos = pos;
+  a.w = w;
+  return a;
+}
+
+// Tokens that the caller has quantized (moe_forward_quantized).
+struct Quantized {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* row_gs;
+};
+
 bool test_fail_requested() {
   const char* v = std::getenv("MOE_FUSED_TEST_FAIL");
   return v != nullptr && v[0] == '1';
@@ -483,6 +521,213 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
   return launch_group_product(p, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
 }
 
+int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, const void* x, int32_t x_rows,
+                     const int32_t* row_ids, int32_t id_div, int32_t M, const uint8_t* w, const uint8_t* w_scales,
+                     const float* gs, int32_t gs_group, int32_t gs_stride, int32_t G, int32_t N, int32_t K,
+                     const int32_t* offsets, int32_t out_dtype, void* out, void* stream) {
+  if (fmt != MOE_FMT_NVFP4 && fmt != MOE_FMT_MXFP4) return MOE_ERR_UNSUPPORTED_FORMAT;
+  if (!known_dtype(x_dtype) || !known_dtype(out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (x_rows < 0 || x_rows > (1 << 26) || M < 0 || M > (1 << 26) || G < 1 || G > 1024) return MOE_ERR_INVALID_ARG;
+  if (N < 1 || N > (1 << 20) || K < 32 || K % 32 != 0 || K > (1 << 20)) return MOE_ERR_INVALID_ARG;
+  if (row_ids != nullptr && id_div < 1) return MOE_ERR_INVALID_ARG;
+  if (swiglu != nullptr) {
+    if (N % 2 != 0) return MOE_ERR_INVALID_ARG;
+    if (swiglu->cap_form < MOE_CAP_SOFT_GATE_UP || swiglu->cap_form > MOE_CAP_NONE) return MOE_ERR_INVALID_ARG;
+    if (swiglu->cap_form != MOE_CAP_NONE && !(swiglu->cap > 0.0f)) return MOE_ERR_INVALID_ARG;
+  }
+  // one workgroup per 16 rows and 64 columns at most, within a launch's 2^32 threads
+  if (((long)G + M / 16) * ceil_div(N, 64) > (1L << 23)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (x_rows == 0 || x == nullptr || w == nullptr || w_scales == nullptr || offsets == nullptr || out == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(w_scales, 4) || !aligned(row_ids, 4) ||
+      !aligned(offsets, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (fmt == MOE_FMT_NVFP4 && (gs == nullptr || !aligned(gs, 4) || gs_group < 1 || N % gs_group != 0 || gs_stride < gs_group))
+    return MOE_ERR_INVALID_ARG;
+  const int st = device_check();
+  if (st != MOE_OK) return st;
+  MatvecArgs a{};
+  a.p.a = static_cast<const uint8_t*>(x);
+  a.p.a_rows = x_rows;
+  a.p.row_ids = row_ids;
+  a.p.id_div = id_div;
+  a.p.M = M;
+  a.p.expect = M;
+  a.p.w = w;
+  a.p.w_sc = w_scales;
+  a.p.G = G;
+  a.p.N = N;
+  a.p.K = K;
+  a.p.offsets = offsets;
+  a.p.out = out;
+  a.p.out_f32 = out_dtype == MOE_DTYPE_F32;
+  a.fmt = fmt;
+  a.dtype = x_dtype;
+  a.gs = gs;
+  a.gs_group = gs_group;
+  a.gs_stride = gs_stride;
+  a.swiglu = swiglu != nullptr;
+  if (swiglu != nullptr) {
+    a.cap_form = swiglu->cap_form;
+    a.cap = swiglu->cap_form == MOE_CAP_NONE ? 1.0f : swiglu->cap;
+  }
+  return launch_group_matvec(a, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_norm_forward(const moe_config* c, int32_t dtype, const void* x, int32_t res_dtype, const void* residual,
+                     int32_t T, int32_t cols, const float* weight, float eps, void* res_out, void* y, float* rstd,
+                     uint8_t* codes, uint8_t* scales, float* row_gs, void* stream) {
+  int st = check_norm(dtype, res_dtype, T, cols);
+  if (st != MOE_OK) return st;
+  if (!(eps > 0.0f && eps <= 3.0e38f)) return MOE_ERR_INVALID_ARG;
+  const bool nv = c != nullptr && c->fmt == MOE_FMT_NVFP4;
+  if (c != nullptr) {
+    if ((st = moe_validate_config(c)) != MOE_OK) return st;
+    if (cols % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (nv && c->act_gs == MOE_ACT_GS_PER_TENSOR) return MOE_ERR_INVALID_ARG;   // needs every row before any code
+  } else if (codes != nullptr || scales != nullptr || row_gs != nullptr) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (T == 0) return MOE_OK;
+  if (x == nullptr || weight == nullptr || (y == nullptr && c == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (c != nullptr && (codes == nullptr || scales == nullptr || (nv && row_gs == nullptr))) return MOE_ERR_INVALID_ARG;
+  const uintptr_t el = element(dtype), rel = element(res_dtype);
+  if (!aligned(x, el) || !aligned(y, el) || !aligned(residual, rel) || !aligned(res_out, rel) || !aligned(weight, 4) ||
+      !aligned(rstd, 4) || !aligned(row_gs, 4) || !aligned(codes, 16))
+    return MOE_ERR_INVALID_ARG;
+  // rows of codes are written from 16-byte reads
+  if (c != nullptr && (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(res_out, 16) ||
+                       !aligned(weight, 16)))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = device_check()) != MOE_OK) return st;
+  NormArgs a{};
+  a.x = x;
+  a.res = residual;
+  a.dtype = dtype;
+  a.res_dtype = residual == nullptr && res_out == nullptr ? dtype : res_dtype;
+  a.T = T;
+  a.cols = cols;
+  a.weight = weight;
+  a.eps = eps;
+  a.res_out = res_out;
+  a.y = y;
+  a.rstd = rstd;
+  if (c != nullptr) {
+    a.fmt = c->fmt;
+    a.codes = codes;
+    a.scales = scales;
+    a.row_gs = row_gs;
+    a.gs_row = c->act_gs != MOE_ACT_GS_STATIC;
+    a.gs_val = c->act_gs_static[0];
+  }
+  return launch_norm_forward(a, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_norm_workspace_size(int32_t T, int32_t cols, size_t* bytes) {
+  const int st = check_norm(MOE_DTYPE_BF16, MOE_DTYPE_BF16, T, cols);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  *bytes = norm_ws_bytes(T, cols);
+  return MOE_OK;
+}
+
+int moe_norm_backward(int32_t dtype, const void* dy, int32_t res_dtype, const void* res, const void* d_res_out,
+                      int32_t T, int32_t cols, const float* weight, const float* rstd, void* d_res, void* dx,
+                      float* d_weight, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_norm(dtype, res_dtype, T, cols);
+  if (st != MOE_OK) return st;
+  if (T == 0 && d_weight == nullptr) return MOE_OK;
+  if (!aligned(d_weight, 4)) return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (dy == nullptr || res == nullptr || weight == nullptr || rstd == nullptr || d_res == nullptr)
+      return MOE_ERR_INVALID_ARG;
+    const uintptr_t el = element(dtype), rel = element(res_dtype);
+    if (!aligned(dy, el) || !aligned(dx, el) || !aligned(res, rel) || !aligned(d_res_out, rel) || !aligned(d_res, rel) ||
+        !aligned(weight, 4) || !aligned(rstd, 4))
+      return MOE_ERR_INVALID_ARG;
+    if (d_weight != nullptr) {
+      if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+      if (ws_bytes < norm_ws_bytes(T, cols)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
+  }
+  if ((st = device_check()) != MOE_OK) return st;
+  NormGradArgs a{};
+  a.dy = dy;
+  a.res = res;
+  a.d_res_out = d_res_out;
+  a.dtype = dtype;
+  a.res_dtype = res_dtype;
+  a.T = T;
+  a.cols = cols;
+  a.weight = weight;
+  a.rstd = rstd;
+  a.d_res = d_res;
+  a.dx = dx;
+  return launch_norm_backward(a, d_weight, ws, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_sort_rows(int32_t dtype, const void* x, int32_t T, int32_t top_k, int32_t cols, const int32_t* pair_pos,
+                  int32_t M, void* out, void* stream) {
+  int st = check_rows(T, top_k, cols, M, pair_pos);
+  if (st != MOE_OK) return st;
+  if (!known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  if (T == 0 || M == 0) return MOE_OK;
+  if (x == nullptr || out == nullptr || !aligned(x, element(dtype)) || !aligned(out, element(dtype)))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = device_check()) != MOE_OK) return st;
+  RowsArgs a = rows_args(T, top_k, cols, M, pair_pos, nullptr);
+  a.token_dtype = a.row_dtype = dtype;
+  a.token = x;
+  a.rows_out = out;
+  return launch_sort_rows(a, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_combine_rows(int32_t y_dtype, const void* y, int32_t M, const int32_t* pair_pos, const float* topk_w,
+                     int32_t T, int32_t top_k, int32_t cols, int32_t out_dtype, void* out, void* stream) {
+  int st = check_rows(T, top_k, cols, M, pair_pos);
+  if (st != MOE_OK) return st;
+  if (!known_dtype(y_dtype) || !known_dtype(out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if ((y == nullptr && M > 0) || out == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned(y, element(y_dtype)) || !aligned(out, element(out_dtype)) || !aligned(topk_w, 4)) return MOE_ERR_INVALID_ARG;
+  if ((st = device_check()) != MOE_OK) return st;
+  RowsArgs a = rows_args(T, top_k, cols, M, pair_pos, topk_w);
+  a.row_dtype = y_dtype;
+  a.token_dtype = out_dtype;
+  a.rows_in = y;
+  a.token_out = out;
+  return launch_combine_rows(a, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
+int moe_sort_rows_backward(int32_t dtype, const void* d_out, int32_t M, const int32_t* pair_pos, int32_t T,
+                           int32_t top_k, int32_t cols, void* dx, void* stream) {
+  return moe_combine_rows(dtype, d_out, M, pair_pos, nullptr, T, top_k, cols, dtype, dx, stream);
+}
+
+int moe_combine_rows_backward(int32_t out_dtype, const void* d_out, int32_t y_dtype, const void* y, int32_t M,
+                              const int32_t* pair_pos, const float* topk_w, int32_t T, int32_t top_k, int32_t cols,
+                              void* dy, float* d_topk_w, void* stream) {
+  int st = check_rows(T, top_k, cols, M, pair_pos);
+  if (st != MOE_OK) return st;
+  if (!known_dtype(y_dtype) || !known_dtype(out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (dy == nullptr && d_topk_w == nullptr) return M > 0 ? MOE_ERR_INVALID_ARG : MOE_OK;   // no rows: dy is empty
+  if (d_out == nullptr || (d_topk_w != nullptr && y == nullptr && M > 0)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(d_out, element(out_dtype)) || !aligned(y, element(y_dtype)) || !aligned(dy, element(y_dtype)) ||
+      !aligned(topk_w, 4) || !aligned(d_topk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = device_check()) != MOE_OK) return st;
+  RowsArgs a = rows_args(T, top_k, cols, M, pair_pos, topk_w);
+  a.token_dtype = out_dtype;
+  a.row_dtype = y_dtype;
+  a.token = d_out;
+  a.rows_in = y;
+  a.rows_out = dy;
+  a.d_w = d_topk_w;
+  return launch_combine_rows_backward(a, static_cast<hipStream_t>(stream)) == 0 ? MOE_OK : MOE_ERR_LAUNCH;
+}
+
 int moe_dispatch(const moe_config* c, const int32_t* topk_ids, int32_t T, int32_t* expert_offsets,
                  int32_t* sorted_pairs, int32_t* pair_pos, void* ws, size_t ws_bytes, void* stream) {
   int st = moe_validate_config(c);
@@ -536,13 +781,18 @@ int moe_prepare_weights(const moe_config* c, const moe_expert_weights* src, moe_
 
 static int forward_impl(const moe_config* c, const void* x, int32_t T, const int32_t* topk_ids,
                         const float* topk_w, const moe_expert_weights* w, void* out, void* ws, size_t ws_bytes,
-                        void* stream, void* const* events, bool fused, bool prep_done = false) {
+                        void* stream, void* const* events, bool fused, bool prep_done = false,
+                        const Quantized* quantized = nullptr) {
   int st = moe_validate_config(c);
   if (st != MOE_OK) return st;
   if (T < 0) return MOE_ERR_INVALID_ARG;
   if ((st = check_ws(c, T, ws, ws_bytes)) != MOE_OK) return st;
   if (T == 0) return MOE_OK;
-  if (x == nullptr || topk_ids == nullptr || topk_w == nullptr || w == nullptr || out == nullptr)
+  if ((x == nullptr && quantized == nullptr) || topk_ids == nullptr || topk_w == nullptr || w == nullptr ||
+      out == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (quantized != nullptr && (quantized->codes == nullptr || quantized->scales == nullptr ||
+                               (c->fmt == MOE_FMT_NVFP4 && quantized->row_gs == nullptr)))
     return MOE_ERR_INVALID_ARG;
   if (w->w13 == nullptr || w->w13_sc == nullptr || w->w2 == nullptr || w->w2_sc == nullptr)
     return MOE_ERR_INVALID_ARG;
@@ -554,11 +804,17 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
       !aligned(w->w13_sc, 4) || !aligned(w->w2_sc, 4) || !aligned(w->gs, 4) || !aligned(topk_ids, 4) ||
       !aligned(topk_w, 4))
     return MOE_ERR_INVALID_ARG;
+  if (quantized != nullptr && (!aligned(quantized->codes, 16) || !aligned(quantized->scales, 16) ||
+                               !aligned(quantized->row_gs, 4)))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_check()) != MOE_OK) return st;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   const Layout L = layout(c, c->max_tokens);
   const int H = c->hidden, F = c->ffn, k = c->top_k, EL = c->num_local_experts;
+  const uint8_t* const xq = quantized != nullptr ? quantized->codes : at<uint8_t>(ws, L.xq);
+  const uint8_t* const xs = quantized != nullptr ? quantized->scales : at<uint8_t>(ws, L.xs);
+  const float* const xg = quantized != nullptr ? quantized->row_gs : at<float>(ws, L.xg);
   const int P = T * k;
   const bool nv = c->fmt == MOE_FMT_NVFP4;
   int bad = 0;
@@ -578,6 +834,12 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
   const ActGs agx = act_gs_of(c, 0, ags), agh = act_gs_of(c, 1, ags);
   if (prep_done) {
     // x quantized and dispatched by moe_route_forward's first launch
+  } else if (quantized != nullptr) {
+    record(events, 2 * MOE_STAGE_QUANT_X, s);
+    record(events, 2 * MOE_STAGE_QUANT_X + 1, s);
+    record(events, 2 * MOE_STAGE_DISPATCH, s);
+    bad |= launch_dispatch(topk_ids, P, c->expert_begin, EL, tile_m, b, s);
+    record(events, 2 * MOE_STAGE_DISPATCH + 1, s);
   } else if (P <= kSmallDispatchPairs && c->fmt != MOE_FMT_MXFP4) {
     // 1 + 2. quantize x per row and dispatch (+ tile list) in one launch; the
     // quantize-x stage covers both, the dispatch stage is empty
@@ -614,8 +876,8 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
     // 3-5. the gate/up product over the dispatched rows, the capped SwiGLU
     // with h's encoding, the down product
     ProductArgs gp{};
-    gp.a = at<uint8_t>(ws, L.xq);
-    gp.a_sc = at<uint8_t>(ws, L.xs);
+    gp.a = xq;
+    gp.a_sc = xs;
     gp.a_rows = T;
     gp.row_ids = b.sorted;
     gp.id_div = k;
@@ -663,9 +925,9 @@ static int forward_impl(const moe_config* c, const void* x, int32_t T, const int
   g.F = F;
   g.k = k;
   g.E_local = EL;
-  g.a_codes = at<uint8_t>(ws, L.xq);
-  g.a_sc = at<uint8_t>(ws, L.xs);
-  g.a_gs = at<float>(ws, L.xg);
+  g.a_codes = xq;
+  g.a_sc = xs;
+  g.a_gs = xg;
   g.w_codes = w->w13;
   g.w_sc = w->w13_sc;
   g.w_gs = w->gs;
@@ -754,6 +1016,13 @@ int moe_forward_fused(const moe_config* c, const void* x, int32_t T, const int32
                       const float* topk_w, const moe_expert_weights* w, void* out, void* ws, size_t ws_bytes,
                       void* stream, void* const* events) {
   return forward_impl(c, x, T, topk_ids, topk_w, w, out, ws, ws_bytes, stream, events, true);
+}
+
+int moe_forward_quantized(const moe_config* c, const uint8_t* codes, const uint8_t* scales, const float* row_gs,
+                          int32_t T, const int32_t* topk_ids, const float* topk_w, const moe_expert_weights* w,
+                          void* out, void* ws, size_t ws_bytes, void* stream, void* const* events) {
+  const Quantized q{codes, scales, row_gs};
+  return forward_impl(c, nullptr, T, topk_ids, topk_w, w, out, ws, ws_bytes, stream, events, false, false, &q);
 }
 
 size_t moe_noalloc_scratch_bytes(void) { return kScratchBytes; }

@@ -1,5 +1,6 @@
 // Launchers of the MXFP4 format (4 in launch_quant, launch_encode_weights and
-// launch_decode_weights), the grouped product and the router's balance loss.
+// launch_decode_weights), the grouped products, the router's balance loss, the
+// residual norm and the sorted rows.
 // Apart from launch.h, whose text the recorded traffic of the older kernels is
 // tied to.
 #pragma once
@@ -68,6 +69,67 @@ struct BalanceArgs {
 size_t balance_ws_bytes(int T, int E, int S);
 int launch_balance_forward(const BalanceArgs& a, hipStream_t stream);
 int launch_balance_backward(const BalanceArgs& a, hipStream_t stream);
+
+// Residual norm (norm.hip).  dtype of x, y, dy, dx; res_dtype of the stream
+// (0 bf16, 1 fp32; a bf16 stream only under bf16 x).
+struct NormArgs {
+  const void* x;            // [T][cols]
+  const void* res;          // [T][cols] nullable
+  int dtype, res_dtype, T, cols;
+  const float* weight;      // [cols]
+  float eps;
+  void* res_out;            // [T][cols] nullable
+  void* y;                  // [T][cols] nullable
+  float* rstd;              // [T] nullable
+  int fmt;                  // 0, or the format of the codes
+  uint8_t* codes;
+  uint8_t* scales;
+  float* row_gs;            // NVFP4
+  int gs_row;               // NVFP4: 1 the row's own scale, 0 gs_val
+  float gs_val;
+};
+struct NormGradArgs {
+  const void* dy;           // [T][cols]
+  const void* res;          // the stream that was normed
+  const void* d_res_out;    // nullable
+  int dtype, res_dtype, T, cols;
+  const float* weight;
+  const float* rstd;
+  void* d_res;
+  void* dx;                 // nullable
+  float* partial;           // set by the launcher
+};
+size_t norm_ws_bytes(int T, int cols);
+int launch_norm_forward(const NormArgs& a, hipStream_t stream);
+int launch_norm_backward(NormGradArgs a, float* d_weight, void* ws, hipStream_t stream);
+
+// Tokens sorted by expert and back (rows.hip).
+struct RowsArgs {
+  int T, k, cols, M;
+  const int32_t* pos;       // [T][k]
+  const float* w;           // [T][k] nullable: all 1
+  int token_dtype, row_dtype;
+  const void* token;        // [T][cols]
+  const void* rows_in;      // [M][cols]
+  void* token_out;
+  void* rows_out;
+  float* d_w;               // [T][k]
+};
+int launch_sort_rows(const RowsArgs& a, hipStream_t stream);
+int launch_combine_rows(const RowsArgs& a, hipStream_t stream);
+int launch_combine_rows_backward(const RowsArgs& a, hipStream_t stream);
+
+// Rows in bf16 or fp32 times 4-bit matrices (matvec.hip).
+struct MatvecArgs {
+  ProductArgs p;            // a: rows of dtype; a_sc unused; N rows of [gate | up] with swiglu
+  int fmt, dtype;           // fmt 1 NVFP4, 4 MXFP4; dtype 0 bf16, 1 fp32
+  const float* gs;          // NVFP4: matrix m of group g at gs[g gs_stride + m]
+  int gs_group, gs_stride;  // matrices of N / gs_group rows in a group
+  int swiglu;               // out [M][N / 2]
+  int cap_form;
+  float cap;
+};
+int launch_group_matvec(const MatvecArgs& a, hipStream_t stream);
 
 // The S split-K planes of router logits added in split order, as the top-k
 // adds them: z [T][E].

@@ -356,6 +356,115 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
                       int32_t G, int32_t N, int32_t K, const int32_t* offsets, int32_t out_dtype, void* out,
                       void* stream);
 
+/* Grouped product of unquantized rows and 4-bit matrices, for the few rows an
+ * expert has in decoding (W4A16): for every group g and row r in
+ * [offsets[g], offsets[g+1])
+ *   out[r][n] = sum_k x[src(r)][k] W[g][n][k],
+ *   src(r) = row_ids == NULL ? r : row_ids[r] / id_div
+ * and with swiglu not NULL, over the gate rows 0 .. N/2-1 and the up rows
+ * N/2 .. N-1 of W[g], the capped SwiGLU of the two (swiglu->cap_form and
+ * ->cap, moe_cap_swiglu's arithmetic; nothing else of it is read): out is
+ * then [M][N/2].
+ *  x [x_rows][K] bf16 or fp32 (x_dtype).  The weights' values enter exactly,
+ *  products are exact, sums fp32, out is fp32 or bf16 (out_dtype, one
+ *  rounding to nearest even).
+ *  fmt: MOE_FMT_NVFP4 or MOE_FMT_MXFP4 (others: MOE_ERR_UNSUPPORTED_FORMAT).
+ *  w [G][N][K/2], w_scales [G][N][K/16] (NVFP4) or [G][N][K/32] (MXFP4),
+ *  canonical, as moe_encode_weights writes them.  NVFP4: the N rows of a
+ *  group are gs_group matrices of N / gs_group rows (N a multiple of
+ *  gs_group), matrix m's fp32 scale at gs[g * gs_stride + m]: for the
+ *  canonical moe_expert_weights w13 with gs, gs_group 2, gs_stride 3; w2 with
+ *  gs + 2, gs_group 1, gs_stride 3.  MXFP4 reads none of the three.  NaN
+ *  scale bytes (E8M0 255, E4M3 0x7F and 0xFF; never written by the encoder)
+ *  give NaN.
+ *  offsets [G+1] ascending, within [0, M] (values outside are clamped); a
+ *  group may be empty.  out: rows in no group are not written.  A row whose
+ *  source lies outside [0, x_rows) is zero.  out may not overlap the inputs.
+ *  K a multiple of 32 up to 2^20, 1 <= N <= 2^20 (even with swiglu), 1 <= G
+ *  <= 1024, M and x_rows at most 2^26, (G + M / 16) ceil(N / 64) at most
+ *  2^23.  x, w and out 16-byte aligned, the other arrays 4.
+ * No workspace; one launch.  Any number of rows is right; what it is made for
+ * is groups of up to 16, each further 16 read the group's weights again. */
+int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, const void* x, int32_t x_rows,
+                     const int32_t* row_ids, int32_t id_div, int32_t M, const uint8_t* w, const uint8_t* w_scales,
+                     const float* gs, int32_t gs_group, int32_t gs_stride, int32_t G, int32_t N, int32_t K,
+                     const int32_t* offsets, int32_t out_dtype, void* out, void* stream);
+
+/* The layer's input in one pass: residual addition, root-mean-square norm
+ * and, with cfg not NULL, the quantization of the normed rows.
+ *   s = x + residual            (in fp32, rounded to res_dtype; x without residual)
+ *   r = 1 / sqrt(mean over the row of s^2 + eps)
+ *   y = s r weight              (in fp32, rounded to dtype)
+ *  x, y [T][cols] of dtype; residual and res_out [T][cols] of res_dtype, which
+ *  is dtype or fp32 (fp32 x with a bf16 stream: MOE_ERR_INVALID_ARG); weight
+ *  [cols] fp32; eps > 0, finite.  residual, res_out (s) and rstd (r, [T]
+ *  fp32) may be NULL, y too where cfg is not.  Outputs may be the inputs of
+ *  the same type (res_out == residual, y == x), not otherwise overlap them.
+ *  cfg: codes, scales and (NVFP4) row_gs of the rows of y as stored, bit for
+ *  bit those of moe_quantize_act at site 0 (layouts there); cols a multiple of
+ *  32; NVFP4 with MOE_ACT_GS_PER_TENSOR, whose scale needs every row first, is
+ *  MOE_ERR_INVALID_ARG.  cfg NULL: the three are NULL.
+ *  0 <= T <= 2^21, 1 <= cols <= 65536.  Arrays aligned to their elements; with
+ *  cfg x, residual, res_out, y, weight and codes 16-byte aligned.  Rows of a
+ *  multiple of 8 elements in 16-byte aligned arrays are read and written 16
+ *  bytes at a time, others element by element.
+ * No workspace; one launch. */
+int moe_norm_forward(const moe_config* cfg, int32_t dtype, const void* x, int32_t res_dtype, const void* residual,
+                     int32_t T, int32_t cols, const float* weight, float eps, void* res_out, void* y, float* rstd,
+                     uint8_t* codes, uint8_t* scales, float* row_gs, void* stream);
+
+/* The norm's gradient: with n = s r, a = dy weight,
+ *   d_res = r (a - n mean over the row of (a n)) + d_res_out
+ *   d_weight[c] = sum over the rows of dy n
+ *  dy [T][cols] of dtype: what reaches y (the codes carry no gradient of
+ *  their own); res [T][cols] of res_dtype: s, moe_norm_forward's res_out, or
+ *  x where there was no residual (res_dtype = dtype); d_res_out [T][cols] of
+ *  res_dtype, may be NULL: what reaches s from further on; rstd [T] the
+ *  forward's.  d_res [T][cols] of res_dtype is the gradient of the residual
+ *  and of x alike; dx, may be NULL, the same of dtype, for an x of another
+ *  type.  d_weight [cols] fp32, may be NULL.  d_res may be d_res_out, or dy
+ *  where the types agree.  The mean square is taken as 1 / r^2.
+ *  ws: moe_norm_workspace_size bytes of device scratch, 256-byte aligned, no
+ *  initial contents needed, for d_weight (else it may be NULL).  Sums are
+ *  fp32 in a fixed order: the same inputs give the same bits.  Sizes and
+ *  alignment as above; one launch, two with d_weight. */
+int moe_norm_workspace_size(int32_t T, int32_t cols, size_t* bytes);
+int moe_norm_backward(int32_t dtype, const void* dy, int32_t res_dtype, const void* res, const void* d_res_out,
+                      int32_t T, int32_t cols, const float* weight, const float* rstd, void* d_res, void* dx,
+                      float* d_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* Token rows to their experts' rows and back.  pair_pos [T][top_k] is
+ * moe_dispatch's: the row of pair (t, j), or a negative number where its
+ * expert is not local; positions outside [0, M) are taken as not local, and
+ * no two pairs may share one.
+ *  moe_sort_rows:          out[pair_pos[t][j]] = x[t]
+ *  moe_sort_rows_backward: dx[t] = sum_j d_out[pair_pos[t][j]]
+ *  moe_combine_rows:       out[t] = sum_j topk_w[t][j] y[pair_pos[t][j]]
+ *  moe_combine_rows_backward:
+ *      dy[pair_pos[t][j]] = topk_w[t][j] d_out[t]
+ *      d_topk_w[t][j] = sum_c d_out[t][c] y[pair_pos[t][j]][c]   (0 if not local)
+ *  x, dx [T][cols] and out, d_out of the sort [M][cols] of dtype; y, dy
+ *  [M][cols] of y_dtype, out, d_out of the combine [T][cols] of out_dtype;
+ *  each bf16 or fp32.  topk_w [T][top_k] fp32, NULL: all 1.  Sums are fp32 in
+ *  slot order over the local pairs, one rounding to nearest even.  Rows of
+ *  the sorted arrays that no pair names are neither read nor written, so what
+ *  lies behind the last local pair plays no part.  dy or d_topk_w may be NULL,
+ *  not both; y may be NULL where d_topk_w is; dy may be y.  Outputs may not
+ *  overlap the inputs otherwise.  d_topk_w is what moe_balance_backward takes.
+ *  0 <= T <= 2^21, 1 <= top_k <= 32, 1 <= cols <= 65536, 0 <= M <= 2^26.
+ *  Arrays aligned to their elements; rows of a multiple of 8 elements in
+ *  16-byte aligned arrays are read and written 16 bytes at a time, others
+ *  element by element.  No workspace; one launch each. */
+int moe_sort_rows(int32_t dtype, const void* x, int32_t T, int32_t top_k, int32_t cols, const int32_t* pair_pos,
+                  int32_t M, void* out, void* stream);
+int moe_sort_rows_backward(int32_t dtype, const void* d_out, int32_t M, const int32_t* pair_pos, int32_t T,
+                           int32_t top_k, int32_t cols, void* dx, void* stream);
+int moe_combine_rows(int32_t y_dtype, const void* y, int32_t M, const int32_t* pair_pos, const float* topk_w,
+                     int32_t T, int32_t top_k, int32_t cols, int32_t out_dtype, void* out, void* stream);
+int moe_combine_rows_backward(int32_t out_dtype, const void* d_out, int32_t y_dtype, const void* y, int32_t M,
+                              const int32_t* pair_pos, const float* topk_w, int32_t T, int32_t top_k, int32_t cols,
+                              void* dy, float* d_topk_w, void* stream);
+
 /* Dispatch of (token, slot) pairs to the local experts: a stable counting
  * sort of the pair ids p = t*k + j by expert id (the "dispatch" stage of the
  * SGLang cookbook's MegaMoE description, section 2).
@@ -412,6 +521,16 @@ int moe_prepare_weights(const moe_config* cfg, const moe_expert_weights* src, mo
 int moe_forward(const moe_config* cfg, const void* x, int32_t T, const int32_t* topk_ids,
                 const float* topk_w, const moe_expert_weights* weights, void* out,
                 void* ws, size_t ws_bytes, void* stream, void* const* events);
+
+/* moe_forward of tokens that are quantized already (moe_norm_forward with a
+ * configuration, moe_quantize_act at site 0): codes [T][...], scales [T][...]
+ * and, for NVFP4, row_gs [T] in cfg->fmt as those calls write them, 16-, 16-
+ * and 4-byte aligned.  The result is moe_forward's on the x that they encode,
+ * bit for bit; the QUANT_X event pair is recorded back to back.  Everything
+ * else as in moe_forward. */
+int moe_forward_quantized(const moe_config* cfg, const uint8_t* codes, const uint8_t* scales, const float* row_gs,
+                          int32_t T, const int32_t* topk_ids, const float* topk_w, const moe_expert_weights* weights,
+                          void* out, void* ws, size_t ws_bytes, void* stream, void* const* events);
 
 /* moe_forward with the expert half in one launch: the single-launch fused
  * MoE of the pages (SGLang blog "SGLang and Miles Add Day-0 Support for

@@ -50,3 +50,4 @@ from .layer import (  # noqa: F401
     quantize_expert_weights, dequantize_expert, cap_swiglu,
 )
 from .balance import balance_forward, balance_backward, balance_loss  # noqa: F401
+from . import stream  # noqa: F401
