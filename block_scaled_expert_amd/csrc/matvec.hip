@@ -26,37 +26,93 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 constexpr int kRows = 16;                 // rows of an item
 constexpr int kLdsBytes = 37 * 1024;      // of x: 4 rows of k 4608 in bf16; four workgroups a CU
 
-// Codes of two blocks of 32 per lane, as loaded (RawW's order), and row r's scales of them.
+// Codes of two blocks of 32 per lane, as loaded (RawW's order), and, unless
+// scales come in fours of chunks (Scales), row r's scales of them.
 template <int FMT>
 struct Chunk {
   v4u q[2];
   uint32_t sc;     // MXFP4: 2 bytes, NVFP4: 4
 };
 
-// ODD: rows of an odd number of 32-blocks; scales are then loaded block by block.
-template <int FMT, bool ODD>
+// WHOLE: rows of whole chunks.  Otherwise the row may end inside a chunk, and
+// scales are loaded block by block.
+template <int FMT, bool WHOLE>
 __device__ inline void load_chunk(Chunk<FMT>& W, Buf wq, Buf ws, const WLane& l, bool on, uint32_t base, uint32_t srow, int c) {
   const int blk = kChunkBlocks * c;
-  const uint32_t off = on && blk + l.at < l.nb ? l.off + base + 16 * blk : kNowhere;
+  const uint32_t off = on && (WHOLE || blk + l.at < l.nb) ? l.off + base + 16 * blk : kNowhere;
   W.q[0] = buf16<true>(wq, off);
   W.q[1] = buf16<true>(wq, off + l.row8);
-  constexpr int S = FMT == 1 ? 2 : 1;      // scale bytes of a block
-  const uint32_t so = S * (srow + blk + kU * l.b);
-  const bool s0 = on && blk + kU * l.b < l.nb, s1 = on && blk + kU * l.b + 1 < l.nb;
-  if constexpr (ODD && FMT == 1) {
-    const uint32_t a = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ws, (int)(s0 ? so : kNowhere), 0, 0);
-    const uint32_t b = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ws, (int)(s1 ? so + 2 : kNowhere), 0, 0);
-    W.sc = a | b << 16;
-  } else if constexpr (FMT == 1) {
-    W.sc = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(ws, (int)(s0 ? so : kNowhere), 0, 0);
-  } else if constexpr (ODD) {
-    const uint32_t a = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)(s0 ? so : kNowhere), 0, 0);
-    const uint32_t b = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)(s1 ? so + 1 : kNowhere), 0, 0);
-    W.sc = a | b << 8;
-  } else {
-    W.sc = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ws, (int)(s0 ? so : kNowhere), 0, 0);
+  if constexpr (!WHOLE) {
+    constexpr int S = FMT == 1 ? 2 : 1;      // scale bytes of a block
+    const uint32_t so = S * (srow + blk + kU * l.b);
+    const uint32_t at0 = on && blk + kU * l.b < l.nb ? so : kNowhere, at1 = on && blk + kU * l.b + 1 < l.nb ? so + S : kNowhere;
+    if constexpr (FMT == 1) {
+      const uint32_t a = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ws, (int)at0, 0, 0);
+      const uint32_t b = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ws, (int)at1, 0, 0);
+      W.sc = a | b << 16;
+    } else {
+      const uint32_t a = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)at0, 0, 0);
+      const uint32_t b = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)at1, 0, 0);
+      W.sc = a | b << 8;
+    }
   }
 }
+
+// Scales of four chunks of 16 rows at a time.  One by one they are 16 (NVFP4)
+// or 8 bytes of a line per row and chunk, and fetching 16 lines for them costs
+// as much as the codes' 16: 512 rows over 283 groups of 4608 x 4608 NVFP4 took
+// 732 us that way, 549 with no scales loaded at all.  Here lane (r, b) loads row
+// r's scales of chunk b (16 or 8 bytes), and swaps between the four rows of
+// lanes hand lane (r, b) what it needs of each chunk.
+template <int FMT>
+struct Scales {
+  v4u next;            // as loaded; MXFP4 uses two words
+  uint32_t now[4];     // of the chunks to come, the nearest first
+
+  // chunks c .. c + 3 of the rows that start at row srow; nw: a row's bytes of a chunk
+  __device__ inline void load(Buf ws, int r, int b, int chunks, bool on, uint32_t row, int c) {
+    constexpr int kBytes = FMT == 1 ? 16 : 8;
+    const uint32_t off = on && c + b < chunks ? kBytes * (row * chunks + c + b) : kNowhere;
+    if constexpr (FMT == 1) {
+      next = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(ws, (int)off, 0, 0));
+    } else {
+      typedef unsigned v2u __attribute__((ext_vector_type(2)));
+      const v2u w = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(ws, (int)off, 0, 0));
+      next[0] = w[0];
+      next[1] = w[1];
+    }
+  }
+  __device__ inline void take(int b) {
+    if constexpr (FMT == 1) {
+      // 4 x 4 words across the rows of lanes: halves, then neighbours
+      const auto a = __builtin_amdgcn_permlane32_swap(next[0], next[2], false, false);
+      const auto c = __builtin_amdgcn_permlane32_swap(next[1], next[3], false, false);
+      const auto e = __builtin_amdgcn_permlane16_swap(a[0], c[0], false, false);
+      const auto f = __builtin_amdgcn_permlane16_swap(a[1], c[1], false, false);
+      now[0] = e[0];
+      now[1] = e[1];
+      now[2] = f[0];
+      now[3] = f[1];
+    } else {
+      // lanes b = 0, 1 share a chunk's first word, 2, 3 its second
+      const auto a = __builtin_amdgcn_permlane32_swap(next[0], next[1], false, false);
+      const auto e = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
+      const auto f = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+      const int half = 16 * (b & 1);
+      now[0] = e[0] >> half;
+      now[1] = e[1] >> half;
+      now[2] = f[0] >> half;
+      now[3] = f[1] >> half;
+    }
+  }
+  __device__ inline uint32_t pop() {
+    const uint32_t s = now[0];
+    now[0] = now[1];
+    now[1] = now[2];
+    now[2] = now[3];
+    return s;
+  }
+};
 
 // Eight codes (low nibble first) as bf16.  MXFP4: scale is 2^(byte - 127), of
 // which the conversion takes the exponent (255 gives NaN).
@@ -96,7 +152,8 @@ __device__ inline void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo
 }  // namespace
 
 // F32: x in fp32.  GLU: tiles of 16 gate and the 16 matching up rows a wave.
-template <int FMT, bool F32, bool GLU, bool ODD>
+// WHOLE: K is a multiple of a chunk.
+template <int FMT, bool F32, bool GLU, bool WHOLE>
 __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
   constexpr int WT = GLU ? 2 : 1, PF = GLU ? 3 : 6, PLANES = F32 ? 3 : 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -131,13 +188,24 @@ __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
   auto load_next = [&](Chunk<FMT> (&W)[WT]) {
 #pragma unroll
     for (int h = 0; h < WT; h++)
-      load_chunk<FMT, ODD>(W[h], wq[h], ws[h], wl, lt < tiles, (uint32_t)lt * (64 * row_bytes),
-                           (uint32_t)(64 * lt + r) * nb, lc);
+      load_chunk<FMT, WHOLE>(W[h], wq[h], ws[h], wl, lt < tiles, (uint32_t)lt * (64 * row_bytes),
+                             (uint32_t)(64 * lt + r) * nb, lc);
     if (++lc == chunks) {
       lc = 0;
       lt++;
     }
   };
+  Scales<FMT> sc[WT];
+  int st = 0, sn = 0;                               // the four chunks whose scales are loaded next
+  auto load_scales = [&]() {
+#pragma unroll
+    for (int h = 0; h < WT; h++) sc[h].load(ws[h], r, b, chunks, st < tiles, 64 * st + r, sn);
+    if ((sn += 4) >= chunks) {
+      sn = 0;
+      st++;
+    }
+  };
+  if constexpr (WHOLE) load_scales();
 #pragma unroll
   for (int j = 0; j < PF; j++) load_next(ring[j]);
 
@@ -198,8 +266,18 @@ __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
           stage_x(c, min(panel, chunks - c));
           lds_barrier();
         }
+        if constexpr (WHOLE) {
+          if (c % 4 == 0) {
+#pragma unroll
+            for (int h = 0; h < WT; h++) sc[h].take(b);
+            load_scales();
+          }
+        }
         RawW raw;
         Frag f[WT];
+        uint32_t scw[WT];
+#pragma unroll
+        for (int h = 0; h < WT; h++) scw[h] = WHOLE ? sc[h].pop() : ring[j][h].sc;
 #pragma unroll
         for (int h = 0; h < WT; h++) {
           raw.q[0] = ring[j][h].q[0];
@@ -217,7 +295,7 @@ __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
               x[e] = *reinterpret_cast<const v8bf*>(mine + e * plane + 2 * kChunkK * pc + 64 * u + 16 * q);
 #pragma unroll
             for (int h = 0; h < WT; h++) {
-              const uint32_t sc = ring[j][h].sc;
+              const uint32_t sc = scw[h];
               const float scale = FMT == 4 ? bits_f((sc >> (8 * u) & 0xFFu) << 23)
                                            : u == 0 ? (q < 2 ? __builtin_amdgcn_cvt_f32_fp8(sc, 0) : __builtin_amdgcn_cvt_f32_fp8(sc, 1))
                                                     : (q < 2 ? __builtin_amdgcn_cvt_f32_fp8(sc, 2) : __builtin_amdgcn_cvt_f32_fp8(sc, 3));
@@ -259,27 +337,27 @@ __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
   }
 }
 
-template <int FMT, bool F32, bool GLU, bool ODD>
+template <int FMT, bool F32, bool GLU, bool WHOLE>
 static void launch_one(const MatvecArgs& a, hipStream_t stream) {
   const int width = GLU ? a.p.N / 2 : a.p.N;
   const long nt = (long)ceil_div(width, 64) * max_tiles(a.p, kRows) / 4096;
   const int NT = (int)(nt < 1 ? 1 : nt > 4 ? 4 : nt);
   const dim3 grid((unsigned)max_tiles(a.p, kRows) * ceil_div(width, 64 * NT));
-  hipLaunchKernelGGL((k_matvec<FMT, F32, GLU, ODD>), grid, dim3(256), kLdsBytes, stream, a, NT);
+  hipLaunchKernelGGL((k_matvec<FMT, F32, GLU, WHOLE>), grid, dim3(256), kLdsBytes, stream, a, NT);
 }
 template <int FMT, bool F32, bool GLU>
-static void launch_odd(const MatvecArgs& a, hipStream_t stream) {
-  if ((a.p.K / 32) % 2) launch_one<FMT, F32, GLU, true>(a, stream);
+static void launch_whole(const MatvecArgs& a, hipStream_t stream) {
+  if (a.p.K % kChunkK == 0) launch_one<FMT, F32, GLU, true>(a, stream);
   else launch_one<FMT, F32, GLU, false>(a, stream);
 }
 template <int FMT>
 static void launch_fmt(const MatvecArgs& a, hipStream_t stream) {
   if (a.dtype == 1) {
-    if (a.swiglu) launch_odd<FMT, true, true>(a, stream);
-    else launch_odd<FMT, true, false>(a, stream);
+    if (a.swiglu) launch_whole<FMT, true, true>(a, stream);
+    else launch_whole<FMT, true, false>(a, stream);
   } else {
-    if (a.swiglu) launch_odd<FMT, false, true>(a, stream);
-    else launch_odd<FMT, false, false>(a, stream);
+    if (a.swiglu) launch_whole<FMT, false, true>(a, stream);
+    else launch_whole<FMT, false, false>(a, stream);
   }
 }
 
