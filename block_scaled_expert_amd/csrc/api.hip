@@ -535,8 +535,8 @@ int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, con
     if (swiglu->cap_form < MOE_CAP_SOFT_GATE_UP || swiglu->cap_form > MOE_CAP_NONE) return MOE_ERR_INVALID_ARG;
     if (swiglu->cap_form != MOE_CAP_NONE && !(swiglu->cap > 0.0f)) return MOE_ERR_INVALID_ARG;
   }
-  // one workgroup per 16 rows and 64 columns at most, within a launch's 2^32 threads
-  if (((long)G + M / 16) * ceil_div(N, 64) > (1L << 23)) return MOE_ERR_INVALID_ARG;
+  // at most one workgroup of 512 threads per 8 rows and 64 columns, within a launch's 2^32 threads
+  if (((long)G + M / 8) * ceil_div(N, 64) > (1L << 22)) return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   if (x_rows == 0 || x == nullptr || w == nullptr || w_scales == nullptr || offsets == nullptr || out == nullptr)
     return MOE_ERR_INVALID_ARG;

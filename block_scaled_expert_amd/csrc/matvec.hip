@@ -6,14 +6,29 @@
 // or, over the gate and up halves of W, the capped SwiGLU of both.
 //
 // The time is that of streaming the weights of the groups that have rows, so
-// the weights go the way of k_product_stream: whole 128-byte lines of 8 rows
-// straight to registers, two rows' halves exchanged there, a ring of chunks that
-// runs on from tile to tile.  A lane then holds 64 consecutive codes of a row.
-// They become bf16 in registers, exactly: an E2M1 value times a power of two
-// (MXFP4, one instruction for two), or times an E4M3 value (NVFP4: at most 6
-// significant bits).  x, in bf16, waits in LDS; an fp32 x as three bf16 parts
-// whose sum it is, so every product is exact and the sums are fp32.  gs is
-// applied to the sums.
+// they go the way of k_product_stream: whole 128-byte lines of 8 rows straight
+// to registers, a ring of chunks that runs on from tile to tile.  What could
+// keep the stream from its rate is the work on each weight, so there is as
+// little of it as can be:
+//  - codes become bf16 two an instruction (E2M1 values are exact there), under
+//    MXFP4 times the block's power of two in the same instruction;
+//  - the products run on v_mfma_f32_4x4x4_16b: a lane multiplies its own codes
+//    (4 of k) with 4 rows of x, and nothing meets another lane's until the tile
+//    is done.  So lanes may hold codes of any row and block, as they were loaded,
+//    and an NVFP4 block's scale is applied to its 4 sums instead of its 16 codes
+//    (0.75 vector instructions a weight; widening and scaling each code for
+//    16x16x32 took 2, and 612 us where this takes 556);
+//  - scales are loaded four chunks at a time (Scales).
+// x, in bf16, waits in LDS; an fp32 x as three bf16 parts whose sum it is.
+// Products are exact and sums fp32; gs is applied to the sums.  A row's sums do
+// not depend on the other rows of its group or call; on how many waves share
+// the chunks they do (KS, from the sizes of the call).
+//
+// Measured (us; TB/s of the weights in use): 64 tokens' gate/up with SwiGLU, 512
+// rows over 283 of 384 groups of 4608 x 4608, NVFP4 556 to 613 on different
+// machines (5.5 to 6.1), MXFP4 549; 192 tokens' down, 1536 rows over 377
+// groups of 4608 x 2304, MXFP4 417 (5.1), with fp32 rows 553 (three times the
+// products and x reads); one token's gate/up, 8 groups, 23.5 (4.1).
 #include "group_product.h"
 
 namespace moe {
@@ -21,10 +36,6 @@ namespace moe {
 namespace {
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef float v2f __attribute__((ext_vector_type(2)));
-
-constexpr int kRows = 16;                 // rows of an item
-constexpr int kLdsBytes = 37 * 1024;      // of x: 4 rows of k 4608 in bf16; four workgroups a CU
 
 // Codes of two blocks of 32 per lane, as loaded (RawW's order), and, unless
 // scales come in fours of chunks (Scales), row r's scales of them.
@@ -69,10 +80,10 @@ struct Scales {
   v4u next;            // as loaded; MXFP4 uses two words
   uint32_t now[4];     // of the chunks to come, the nearest first
 
-  // chunks c .. c + 3 of the rows that start at row srow; nw: a row's bytes of a chunk
-  __device__ inline void load(Buf ws, int r, int b, int chunks, bool on, uint32_t row, int c) {
+  // this lane's chunk: number `at` of the view's, row after row
+  __device__ inline void load(Buf ws, bool on, uint32_t at) {
     constexpr int kBytes = FMT == 1 ? 16 : 8;
-    const uint32_t off = on && c + b < chunks ? kBytes * (row * chunks + c + b) : kNowhere;
+    const uint32_t off = on ? kBytes * at : kNowhere;
     if constexpr (FMT == 1) {
       next = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(ws, (int)off, 0, 0));
     } else {
@@ -114,23 +125,37 @@ struct Scales {
   }
 };
 
-// Eight codes (low nibble first) as bf16.  MXFP4: scale is 2^(byte - 127), of
-// which the conversion takes the exponent (255 gives NaN).
-template <int FMT>
-__device__ inline v8bf widen(uint32_t w, float scale) {
-  if constexpr (FMT == 4) {
-    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
-    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
-    return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-  } else {
-    const v2f a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const v2f c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    const v2bf e = __builtin_convertvector((v2f{a[0] * scale, a[1] * scale}), v2bf);
-    const v2bf f = __builtin_convertvector((v2f{b[0] * scale, b[1] * scale}), v2bf);
-    const v2bf g = __builtin_convertvector((v2f{c[0] * scale, c[1] * scale}), v2bf);
-    const v2bf h = __builtin_convertvector((v2f{d[0] * scale, d[1] * scale}), v2bf);
-    return v8bf{e[0], e[1], f[0], f[1], g[0], g[1], h[0], h[1]};
+// Eight codes (low nibble first) as bf16, times the power of two in scale's
+// exponent (an E8M0 byte moved there: 255 gives NaN).
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+__device__ inline v8s widen(uint32_t w, float scale) {
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+  return __builtin_bit_cast(v8s, v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]});
+}
+__device__ inline v4s lo4(v8s v) { return v4s{v[0], v[1], v[2], v[3]}; }
+__device__ inline v4s hi4(v8s v) { return v4s{v[4], v[5], v[6], v[7]}; }
+
+// Lane (r, b) of 16 x 4: the sums over the lanes that agree modulo 8, of value
+// b of s[0] where r < 8 and of s[1] elsewhere.
+__device__ inline float lanes_by_8(const v4f (&s)[2], int r) {
+  float k[4];
+#pragma unroll
+  for (int m = 0; m < 4; m++) {
+    const float away = r < 8 ? s[1][m] : s[0][m];
+    k[m] = (r < 8 ? s[0][m] : s[1][m]) +
+           bits_f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f_bits(away), 0x128, 0xF, 0xF, false));   // row_ror:8
   }
+  // values 0, 1 to the lower half of the lanes, 2, 3 to the upper; then the odd ones to odd rows
+  float h[2];
+#pragma unroll
+  for (int m = 0; m < 2; m++) {
+    const auto w = __builtin_amdgcn_permlane32_swap(f_bits(k[m]), f_bits(k[m + 2]), false, false);
+    h[m] = bits_f(w[0]) + bits_f(w[1]);
+  }
+  const auto w = __builtin_amdgcn_permlane16_swap(f_bits(h[0]), f_bits(h[1]), false, false);
+  return bits_f(w[0]) + bits_f(w[1]);
 }
 
 // x as hi + mid + lo, each a bf16 (the upper 16 bits of what is left); inf and
@@ -151,56 +176,64 @@ __device__ inline void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo
 
 }  // namespace
 
-// F32: x in fp32.  GLU: tiles of 16 gate and the 16 matching up rows a wave.
-// WHOLE: K is a multiple of a chunk.
-template <int FMT, bool F32, bool GLU, bool WHOLE>
-__global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
-  constexpr int WT = GLU ? 2 : 1, PF = GLU ? 3 : 6, PLANES = F32 ? 3 : 1;
+// F32: x in fp32.  GLU: the upper half of the waves takes the up rows of the
+// columns that the lower half takes the gate rows of.  WHOLE: K is a multiple of
+// a chunk.  NQ: quads of x rows of an item.  KS sets of WC waves take every KS-th
+// chunk each; with KS > 1 an item is one tile, and all of x fits in LDS.
+template <int FMT, bool F32, bool GLU, bool WHOLE, int NQ>
+__global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, int KS, int lds_bytes) {
+  constexpr int PF = 3, PLANES = F32 ? 3 : 1, kRows = 4 * NQ;   // PF 4: 1-2% slower, 6: 3-4%
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int src[kRows];
+  __shared__ float up[GLU ? 2 : 1][4][NQ][64];      // sums of up rows on their way to the gate's waves
+  __shared__ Item item;
   const ProductArgs& p = a.p;
   const int width = GLU ? p.N / 2 : p.N;            // columns of out
+  const int cols = GLU ? 8 * WC : 16 * WC;          // of a tile
 
-  Item it;
-  if (!find_item<kRows>(p, (width + 64 * NT - 1) / (64 * NT), blockIdx.x, it)) return;
-  const int g = it.g, m0 = it.row0, rows = it.rows, n0 = it.bx * 64 * NT;
-
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int r = lane & 15, b = lane >> 4;
-  const int nb = p.K / 32, chunks = (nb + kChunkBlocks - 1) / kChunkBlocks;
-  const int tiles = min(NT, (width - n0 + 63) / 64);
-  const int row_bytes = p.K / 2, sc_bytes = nb * (FMT == 1 ? 2 : 1);
-  // this wave's weight rows nw + 64 t ..; rows past the width read zeros
-  const int nw = n0 + 16 * wave;
-  const int wrows = max(min(64 * NT - 16 * wave, width - nw), 0);
-  Buf wq[WT], ws[WT];
-#pragma unroll
-  for (int h = 0; h < WT; h++) {
-    const size_t at = (size_t)g * p.N + (size_t)h * width + min(nw, width - 1);
-    wq[h] = make_buf(p.w + at * row_bytes, wrows * row_bytes);
-    ws[h] = make_buf(p.w_sc + at * sc_bytes, wrows * sc_bytes);
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, threads = blockDim.x;
+  if (wave == 0) {                                  // one wave looks for the item
+    Item it;
+    if (!find_item<kRows>(p, (width + cols * NT - 1) / (cols * NT), blockIdx.x, it)) it.rows = 0;
+    if (lane == 0) item = it;
   }
+  lds_barrier();
+  const int rows = __builtin_amdgcn_readfirstlane(item.rows);
+  if (rows == 0) return;
+  const int g = __builtin_amdgcn_readfirstlane(item.g), m0 = __builtin_amdgcn_readfirstlane(item.row0);
+  const int n0 = __builtin_amdgcn_readfirstlane(item.bx) * cols * NT;
+
+  const int r = lane & 15, b = lane >> 4;
+  const int part = wave / WC, col = wave - part * WC;   // of the chunks, of the tile's columns
+  const int half = GLU && 2 * col >= WC ? 1 : 0, pair = GLU ? col - half * (WC / 2) : col;
+  const int nb = p.K / 32, chunks = (nb + kChunkBlocks - 1) / kChunkBlocks;
+  const int mine = (chunks - part + KS - 1) / KS;   // chunks part, part + KS, ..
+  const int tiles = min(NT, (width - n0 + cols - 1) / cols);
+  const int row_bytes = p.K / 2, sc_bytes = nb * (FMT == 1 ? 2 : 1);
+  // this wave's weight rows nw + cols t ..; rows past the width read zeros
+  const int nw = n0 + 16 * pair;
+  const int wrows = max(min(cols * NT - 16 * pair, width - nw), 0);
+  const size_t wr0 = (size_t)g * p.N + (size_t)half * width + min(nw, width - 1);
+  const Buf wq = make_buf(p.w + wr0 * row_bytes, wrows * row_bytes);
+  const Buf ws = make_buf(p.w_sc + wr0 * sc_bytes, wrows * sc_bytes);
   const WLane wl(r, b, row_bytes, nb);
 
   if (tid < kRows) src[tid] = tid < rows ? source_row(p, m0 + tid) : -1;
-  Chunk<FMT> ring[PF][WT];
-  int lt = 0, lc = 0;                               // the chunk that is loaded next
-  auto load_next = [&](Chunk<FMT> (&W)[WT]) {
-#pragma unroll
-    for (int h = 0; h < WT; h++)
-      load_chunk<FMT, WHOLE>(W[h], wq[h], ws[h], wl, lt < tiles, (uint32_t)lt * (64 * row_bytes),
-                             (uint32_t)(64 * lt + r) * nb, lc);
-    if (++lc == chunks) {
-      lc = 0;
+  Chunk<FMT> ring[PF];
+  int lt = mine > 0 ? 0 : tiles, li = 0;            // the chunk that is loaded next
+  auto load_next = [&](Chunk<FMT>& W) {
+    load_chunk<FMT, WHOLE>(W, wq, ws, wl, lt < tiles, (uint32_t)lt * (cols * row_bytes), (uint32_t)(cols * lt + r) * nb,
+                           part + KS * li);
+    if (++li == mine) {
+      li = 0;
       lt++;
     }
   };
-  Scales<FMT> sc[WT];
-  int st = 0, sn = 0;                               // the four chunks whose scales are loaded next
+  Scales<FMT> sc;
+  int st = lt, sn = 0;                              // the four chunks whose scales are loaded next
   auto load_scales = [&]() {
-#pragma unroll
-    for (int h = 0; h < WT; h++) sc[h].load(ws[h], r, b, chunks, st < tiles, 64 * st + r, sn);
-    if ((sn += 4) >= chunks) {
+    sc.load(ws, st < tiles && sn + b < mine, (uint32_t)(cols * st + r) * chunks + part + KS * (sn + b));
+    if ((sn += 4) >= mine) {
       sn = 0;
       st++;
     }
@@ -211,15 +244,23 @@ __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
 
   // x in panels of as many chunks as the item's rows leave room for; rows are
   // 16 bytes apart beyond a multiple of 512, which spreads them over the banks
-  const int most = max((kLdsBytes / (PLANES * rows) - 16) / (2 * kChunkK), 1);
+  const int most = max((lds_bytes / (PLANES * rows) - 16) / (2 * kChunkK), 1);
   const int panels = (chunks + most - 1) / most, panel = (chunks + panels - 1) / panels;
   const int stride = 2 * kChunkK * panel + 16, plane = stride * rows;
   auto stage_x = [&](int p0, int pn) {
-    const int pieces = pn * (kChunkK / 8);          // of 8 k
-    for (int i = tid; i < rows * pieces; i += 256) {
-      const int row = i / pieces, q = i - row * pieces, k = kChunkK * p0 + 8 * q, s = max(src[row], 0);
+    // a wave per row and run of 512 k (64 pieces of 8), if there are enough
+    const int runs = (pn + 1) / 2, waves = threads >> 6;
+    int row = wave, run = 0;
+    for (;;) {
+      while (row >= rows) {
+        row -= rows;
+        run++;
+      }
+      if (run >= runs) break;
+      const int q = 64 * run + lane, k = kChunkK * p0 + 8 * q, s = max(src[row], 0);
+      const bool in = q < pn * (kChunkK / 8);
       v4u hi = v4u{0, 0, 0, 0}, mid = hi, lo = hi;
-      if (k < p.K) {                                // zeros past the end of k
+      if (in && (WHOLE || k < p.K)) {               // zeros past the end of k
         if constexpr (F32) {
           const v4f* x = reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(p.a) + (size_t)s * p.K + k);
           const v4f u = x[0], v = x[1];
@@ -237,11 +278,14 @@ __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
         }
       }
       uint8_t* const to = lds + row * stride + 16 * q;
-      *reinterpret_cast<v4u*>(to) = hi;
-      if constexpr (F32) {
-        *reinterpret_cast<v4u*>(to + plane) = mid;
-        *reinterpret_cast<v4u*>(to + 2 * plane) = lo;
+      if (in) {
+        *reinterpret_cast<v4u*>(to) = hi;
+        if constexpr (F32) {
+          *reinterpret_cast<v4u*>(to + plane) = mid;
+          *reinterpret_cast<v4u*>(to + 2 * plane) = lo;
+        }
       }
+      row += waves;
     }
   };
   lds_barrier();                                    // src is written
@@ -250,100 +294,177 @@ __global__ __launch_bounds__(256, 4) void k_matvec(MatvecArgs a, int NT) {
     stage_x(0, chunks);
     lds_barrier();
   }
-  // rows past the item read its last one; a row's outputs depend on that row alone
-  const uint8_t* const mine = lds + min(r, rows - 1) * stride + 128 * b;
-
-  v4f acc[WT];
+  // lane (r, b) of quad k has x row 4 k + r % 4 and the block of 32 that it has codes of;
+  // past the item its last row; a row's outputs depend on that row alone
+  int x_at[NQ];
 #pragma unroll
-  for (int h = 0; h < WT; h++) acc[h] = v4f{0, 0, 0, 0};
-  int t = 0, c = 0, pc = 0;                         // tile, chunk, chunk within the panel
+  for (int k = 0; k < NQ; k++) x_at[k] = min(4 * k + (r & 3), rows - 1) * stride + 128 * b + 64 * (r >> 3);
+
+  v4f acc[NQ][2];                                   // of weight rows r % 8 and 8 + r % 8
+  auto clear = [&]() {
+#pragma unroll
+    for (int k = 0; k < NQ; k++) acc[k][0] = acc[k][1] = v4f{0, 0, 0, 0};
+  };
+  clear();
+  // lane (r, b) puts out weight row r and x rows b, 4 + b, ..
+  auto finish = [&](int t) {
+    const int n = nw + cols * t + r;
+    float v[NQ];
+#pragma unroll
+    for (int k = 0; k < NQ; k++) {
+      if (4 * k >= rows) continue;
+      v[k] = lanes_by_8(acc[k], r);
+      if constexpr (FMT == 1)
+        v[k] *= a.gs[(size_t)g * a.gs_stride + (half * width + min(n, width - 1)) / (p.N / a.gs_group)];
+    }
+    if constexpr (GLU) {                            // two tiles' worth of room: one barrier a tile
+      if (half)
+#pragma unroll
+        for (int k = 0; k < NQ; k++) up[t & 1][pair][k][lane] = v[k];
+      lds_barrier();
+      if (half) return;
+    }
+    if (n >= width) return;
+#pragma unroll
+    for (int k = 0; k < NQ; k++) {
+      const int m = 4 * k + b;
+      if (m < rows) {
+        float o = v[k];
+        if constexpr (GLU) o = cap_swiglu(o, up[t & 1][pair][k][lane], a.cap_form, a.cap, 1.0f / a.cap);
+        o = src[m] < 0 ? 0.0f : o;
+        const size_t i = (size_t)(m0 + m) * width + n;
+        if (p.out_f32) static_cast<float*>(p.out)[i] = o;
+        else static_cast<__bf16*>(p.out)[i] = (__bf16)o;   // to nearest even
+      }
+    }
+  };
+  int t = mine > 0 ? 0 : tiles, i = 0, xc = part;   // tile, chunk of mine, chunk within the panel
   while (t < tiles) {
 #pragma unroll
     for (int j = 0; j < PF; j++) {
       if (t < tiles) {
-        if (!one && pc == 0) {                      // every wave is at the same chunk
+        if (!one && xc == 0) {                      // KS is 1: every wave is at the same chunk
           lds_barrier();                            // the last panel has been read
-          stage_x(c, min(panel, chunks - c));
+          stage_x(i, min(panel, chunks - i));
           lds_barrier();
         }
         if constexpr (WHOLE) {
-          if (c % 4 == 0) {
-#pragma unroll
-            for (int h = 0; h < WT; h++) sc[h].take(b);
+          if (i % 4 == 0) {
+            sc.take(b);
             load_scales();
           }
         }
-        RawW raw;
-        Frag f[WT];
-        uint32_t scw[WT];
+        // this lane's block of 32: its scales in weight rows r % 8 and 8 + r % 8
+        const uint32_t own = WHOLE ? sc.pop() : ring[j].sc;
+        const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)own, 0x128, 0xF, 0xF, false);   // row_ror:8
+        constexpr int kHalf = FMT == 1 ? 16 : 8;
+        const uint32_t s0 = r < 8 ? own : other >> kHalf, s1 = r < 8 ? other : own >> kHalf;
+        const uint8_t* const xp = lds + 2 * kChunkK * xc;
 #pragma unroll
-        for (int h = 0; h < WT; h++) scw[h] = WHOLE ? sc[h].pop() : ring[j][h].sc;
+        for (int e = 0; e < 2; e++) {               // 16 of k: an NVFP4 block
+          v8s w[2][2];
+          float scale[2];
 #pragma unroll
-        for (int h = 0; h < WT; h++) {
-          raw.q[0] = ring[j][h].q[0];
-          raw.q[1] = ring[j][h].q[1];
-          raw.sc = 0;
-          operand_w<false>(raw, f[h]);
-        }
+          for (int y = 0; y < 2; y++) {
+            const uint32_t s = y == 0 ? s0 : s1;
+            scale[y] = FMT == 4 ? bits_f((s & 0xFFu) << 23)
+                                : e == 0 ? __builtin_amdgcn_cvt_f32_fp8(s, 0) : __builtin_amdgcn_cvt_f32_fp8(s, 1);
 #pragma unroll
-        for (int u = 0; u < kU; u++) {
-#pragma unroll
-          for (int q = 0; q < 4; q++) {
-            v8bf x[PLANES];
-#pragma unroll
-            for (int e = 0; e < PLANES; e++)
-              x[e] = *reinterpret_cast<const v8bf*>(mine + e * plane + 2 * kChunkK * pc + 64 * u + 16 * q);
-#pragma unroll
-            for (int h = 0; h < WT; h++) {
-              const uint32_t sc = scw[h];
-              const float scale = FMT == 4 ? bits_f((sc >> (8 * u) & 0xFFu) << 23)
-                                           : u == 0 ? (q < 2 ? __builtin_amdgcn_cvt_f32_fp8(sc, 0) : __builtin_amdgcn_cvt_f32_fp8(sc, 1))
-                                                    : (q < 2 ? __builtin_amdgcn_cvt_f32_fp8(sc, 2) : __builtin_amdgcn_cvt_f32_fp8(sc, 3));
-              const v8bf wv = widen<FMT>(f[h].q[u][q], scale);
-#pragma unroll
-              for (int e = PLANES - 1; e >= 0; e--) acc[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[e], wv, acc[h], 0, 0, 0);
-            }
+            for (int q = 0; q < 2; q++) w[y][q] = widen(ring[j].q[y][2 * e + q], FMT == 4 ? scale[y] : 1.0f);
           }
-        }
-        pc = pc + 1 == panel ? 0 : pc + 1;
-        if (++c == chunks) {                        // the tile is done
-          const int n = nw + 64 * t + r;
-          if (n < width) {
-            float gs[WT];
 #pragma unroll
-            for (int h = 0; h < WT; h++)
-              gs[h] = FMT == 1 ? a.gs[(size_t)g * a.gs_stride + (h * width + n) / (p.N / a.gs_group)] : 1.0f;
+          for (int k = 0; k < NQ; k++) {
+            if (k > 0 && 4 * k >= rows) continue;
+            v8s x[PLANES][2];
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-              const int m = 4 * b + q;
-              if (m < rows) {
-                float v = acc[0][q] * gs[0];
-                if constexpr (GLU) v = cap_swiglu(v, acc[1][q] * gs[1], a.cap_form, a.cap, 1.0f / a.cap);
-                v = src[m] < 0 ? 0.0f : v;
-                const size_t i = (size_t)(m0 + m) * width + n;
-                if (p.out_f32) static_cast<float*>(p.out)[i] = v;
-                else static_cast<__bf16*>(p.out)[i] = (__bf16)v;   // to nearest even
+            for (int d = 0; d < PLANES; d++)
+#pragma unroll
+              for (int q = 0; q < 2; q++) x[d][q] = *reinterpret_cast<const v8s*>(xp + x_at[k] + d * plane + 32 * e + 16 * q);
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+              v4f c = FMT == 4 ? acc[k][y] : v4f{0, 0, 0, 0};
+#pragma unroll
+              for (int q = 0; q < 2; q++)
+#pragma unroll
+                for (int d = PLANES - 1; d >= 0; d--) {
+                  c = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(lo4(x[d][q]), lo4(w[y][q]), c, 0, 0, 0);
+                  c = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(hi4(x[d][q]), hi4(w[y][q]), c, 0, 0, 0);
+                }
+              if constexpr (FMT == 4) {
+                acc[k][y] = c;
+              } else {
+#pragma unroll
+                for (int m = 0; m < 4; m++) acc[k][y][m] = fmaf(scale[y], c[m], acc[k][y][m]);
               }
             }
           }
-#pragma unroll
-          for (int h = 0; h < WT; h++) acc[h] = v4f{0, 0, 0, 0};
-          c = pc = 0;
+        }
+        xc = !one && xc + 1 == panel ? 0 : xc + KS;
+        if (++i == mine) {                          // the tile is done
+          if (KS == 1) {
+            finish(t);
+            clear();
+          }
+          i = 0;
+          xc = part;
           t++;
         }
       }
       load_next(ring[j]);
     }
   }
+  if (KS > 1) {                                     // the parts' sums, in order
+    v4f* const red = reinterpret_cast<v4f*>(lds);   // [KS - 1][WC][NQ][2][64]
+    lds_barrier();                                  // x has been read
+    if (part > 0)
+#pragma unroll
+      for (int k = 0; k < NQ; k++)
+#pragma unroll
+        for (int y = 0; y < 2; y++) red[((((part - 1) * WC + col) * NQ + k) * 2 + y) * 64 + lane] = acc[k][y];
+    lds_barrier();
+    if (part > 0) return;
+    for (int e = 0; e < KS - 1; e++)
+#pragma unroll
+      for (int k = 0; k < NQ; k++)
+#pragma unroll
+        for (int y = 0; y < 2; y++) acc[k][y] += red[(((e * WC + col) * NQ + k) * 2 + y) * 64 + lane];
+    finish(0);
+  }
 }
 
+// Rows of an item: 8.  With 16 the registers for their sums cost 2 to 5% where
+// groups have 1 to 4 rows; with 4 groups of 4 rows on average took 499 us where
+// 8 take 416.
+constexpr int kQuads = 2;
+
+// Waves of a workgroup and LDS, by tiles (64 columns of 8 rows at most):
+//  - up to 10240, 4 waves and 36 KiB, four workgroups a CU: with 8 waves and 76
+//    KiB the same work is handed out in larger pieces, which took 84 us instead
+//    of 68 for 4 tokens' gate/up, 229 instead of 219 for 16;
+//  - above, 8 waves and 76 KiB, in which 8 rows of k 4608 fit: where groups have
+//    more than 3 rows, 4 waves bring x in again for every tile (1536 rows down
+//    in fp32 624 us instead of 553, gate/up 882 instead of 842);
+//  - up to 256, where all of x fits, two sets of 2 waves share the chunks, up to
+//    128 four sets: there are not enough columns to go round (4608 x 4608, one
+//    row: 8.7 us instead of 11.8; 16384 columns 12.9 instead of 13.7).
 template <int FMT, bool F32, bool GLU, bool WHOLE>
 static void launch_one(const MatvecArgs& a, hipStream_t stream) {
-  const int width = GLU ? a.p.N / 2 : a.p.N;
-  const long nt = (long)ceil_div(width, 64) * max_tiles(a.p, kRows) / 4096;
+  const int width = GLU ? a.p.N / 2 : a.p.N, items = max_tiles(a.p, 4 * kQuads), chunks = ceil_div(a.p.K, kChunkK);
+  const long tiles = (long)ceil_div(width, GLU ? 32 : 64) * items;
+  int WC = tiles <= 10240 ? 4 : 8, KS = 1, lds = (WC == 8 ? 76 : 36) * 1024;
+  // tiles a workgroup takes in turn, so that there remain about 1024 workgroups (2 to 4 a CU)
+  const long nt = tiles * 4 / WC / 1024;
   const int NT = (int)(nt < 1 ? 1 : nt > 4 ? 4 : nt);
-  const dim3 grid((unsigned)max_tiles(a.p, kRows) * ceil_div(width, 64 * NT));
-  hipLaunchKernelGGL((k_matvec<FMT, F32, GLU, WHOLE>), grid, dim3(256), kLdsBytes, stream, a, NT);
+  const int most = a.p.M < 4 * kQuads ? a.p.M : 4 * kQuads;   // rows of an item at most
+  const long need = (long)(F32 ? 3 : 1) * most * (2 * kChunkK * chunks + 16);
+  if (tiles <= 256 && need <= 80 * 1024 && chunks > 1) {
+    WC = 2;
+    KS = tiles <= 128 && chunks > 3 ? 4 : 2;
+    const int red = (KS - 1) * WC * kQuads * 2048;
+    lds = need > red ? (int)need : red;
+  }
+  const dim3 grid((unsigned)items * ceil_div(width, (GLU ? 8 : 16) * WC * NT));
+  hipLaunchKernelGGL((k_matvec<FMT, F32, GLU, WHOLE, kQuads>), grid, dim3(64 * WC * KS), lds, stream, a, NT, WC, KS, lds);
 }
 template <int FMT, bool F32, bool GLU>
 static void launch_whole(const MatvecArgs& a, hipStream_t stream) {

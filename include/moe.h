@@ -381,10 +381,10 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
  *  group may be empty.  out: rows in no group are not written.  A row whose
  *  source lies outside [0, x_rows) is zero.  out may not overlap the inputs.
  *  K a multiple of 32 up to 2^20, 1 <= N <= 2^20 (even with swiglu), 1 <= G
- *  <= 1024, M and x_rows at most 2^26, (G + M / 16) ceil(N / 64) at most
- *  2^23.  x, w and out 16-byte aligned, the other arrays 4.
+ *  <= 1024, M and x_rows at most 2^26, (G + M / 8) ceil(N / 64) at most
+ *  2^22.  x, w and out 16-byte aligned, the other arrays 4.
  * No workspace; one launch.  Any number of rows is right; what it is made for
- * is groups of up to 16, each further 16 read the group's weights again. */
+ * is groups of up to 8, each further 8 read the group's weights again. */
 int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, const void* x, int32_t x_rows,
                      const int32_t* row_ids, int32_t id_div, int32_t M, const uint8_t* w, const uint8_t* w_scales,
                      const float* gs, int32_t gs_group, int32_t gs_stride, int32_t G, int32_t N, int32_t K,
