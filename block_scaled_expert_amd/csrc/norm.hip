@@ -28,7 +28,7 @@ __device__ inline float lanes_max(float v) {
     v = fmaxf(v, bits_f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f_bits(v), 0x4E, 0xF, 0xF, false)));
   return v;
 }
-__device__ inline float amax8(const float (&v)[8]) {
+__device__ inline float amax8(const float* v) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[i]));   // a NaN is passed over
@@ -37,7 +37,7 @@ __device__ inline float amax8(const float (&v)[8]) {
 
 // This lane's 8 elements of a row as MXFP8 (2) or MXFP4 (4); a block of 32 is 4 lanes'.
 template <int FMT>
-__device__ inline void encode_mx(float (&v)[8], int c, uint8_t* codes, uint8_t* scales, bool on) {
+__device__ inline void encode_mx(float* v, int c, uint8_t* codes, uint8_t* scales, bool on) {
   const float am = lanes_max<4>(amax8(v));
   const int E = FMT == 2 ? mx_exponent(am) : mxfp4_exponent(am);
   const float step = pow2f(-E);
@@ -55,7 +55,7 @@ __device__ inline void encode_mx(float (&v)[8], int c, uint8_t* codes, uint8_t* 
 }
 
 // The same as NVFP4 under the row's scale gs; a block of 16 is 2 lanes'.
-__device__ inline void encode_nv(const float (&v)[8], int c, float gs, bool zero_row, uint8_t* codes, uint8_t* scales,
+__device__ inline void encode_nv(const float* v, int c, float gs, bool zero_row, uint8_t* codes, uint8_t* scales,
                                  bool on) {
 #pragma clang fp contract(off)
   const float ab = lanes_max<2>(amax8(v));
@@ -90,62 +90,52 @@ __device__ inline float group_amax(float v, float* red) {
 
 }  // namespace
 
-// One workgroup per row; lane chunk c = thread + blockDim i, i < CH.  RT: the
-// stream's type.  FMT: 0 no codes.
-template <typename XT, typename RT, int FMT, bool VEC, int CH>
+// One workgroup per row.  RT: the stream's type.  FMT: 0 no codes.
+template <typename XT, typename RT, int FMT, bool FULL, int CH, bool NT>
 __global__ __launch_bounds__(1024) void k_norm_forward(NormArgs a) {
   __shared__ float red[2][16];
-  const int tid = threadIdx.x, nt = blockDim.x, cols = a.cols;
-  const size_t row = blockIdx.x;
-  const XT* const x = static_cast<const XT*>(a.x) + row * cols;
-  const RT* const res = a.res == nullptr ? nullptr : static_cast<const RT*>(a.res) + row * cols;
+  typedef Span<FULL, CH> S;
+  const S sp(a.cols, blockDim.x);
+  const int cols = a.cols;
+  const size_t at = (size_t)blockIdx.x * cols;
+  const RT* const res = static_cast<const RT*>(a.res);
 
-  Raw8<XT> rx[CH];
-  Raw8<RT> rr[CH];
-#pragma unroll
-  for (int i = 0; i < CH; i++) load_raw8<VEC>(rx[i], x, tid + nt * i, cols);
+  typename S::template Raw<XT> rx;
+  typename S::template Raw<RT> rr;
+  sp.template load<NT>(rx, static_cast<const XT*>(a.x) + at);
+  if (res != nullptr) sp.template load<NT>(rr, res + at);
+  float v[S::N], ss = 0.0f;
+  sp.get(rx, v);
   if (res != nullptr) {
+    float u[S::N];
+    sp.get(rr, u);
 #pragma unroll
-    for (int i = 0; i < CH; i++) load_raw8<VEC>(rr[i], res, tid + nt * i, cols);
+    for (int k = 0; k < S::N; k++) v[k] = stored<RT>(v[k] + u[k]);
   }
-  float v[CH][8], ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < CH; i++) {
-    const int c = tid + nt * i;
-    rx[i].get(v[i]);
-    if (res != nullptr) {
-      float u[8];
-      rr[i].get(u);
-#pragma unroll
-      for (int e = 0; e < 8; e++) v[i][e] = stored<RT>(v[i][e] + u[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      v[i][e] = in_row<VEC>(c, e, cols) ? v[i][e] : 0.0f;
-      ss = fmaf(v[i][e], v[i][e], ss);
-    }
-    if (a.res_out != nullptr) store8<VEC>(static_cast<RT*>(a.res_out) + row * cols, c, cols, v[i]);
+  for (int k = 0; k < S::N; k++) {
+    v[k] = sp.has(k) ? v[k] : 0.0f;
+    ss = fmaf(v[k], v[k], ss);
   }
+  if (a.res_out != nullptr) sp.template put<NT>(static_cast<RT*>(a.res_out) + at, v);
+  typename S::template Raw<float> rw;
+  sp.load(rw, a.weight);
   ss = group_total(ss, red[0]);
   const float rstd = 1.0f / sqrtf(ss / (float)cols + a.eps);
-  if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
+  if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
 
+  float w[S::N];
+  sp.get(rw, w);
 #pragma unroll
-  for (int i = 0; i < CH; i++) {
-    const int c = tid + nt * i;
-    Raw8<float> rw;
-    load_raw8<VEC>(rw, a.weight, c, cols);
-    float w[8];
-    rw.get(w);
-#pragma unroll
-    for (int e = 0; e < 8; e++) v[i][e] = stored<XT>(v[i][e] * rstd * w[e]);
-    if (a.y != nullptr) store8<VEC>(static_cast<XT*>(a.y) + row * cols, c, cols, v[i]);
-  }
+  for (int k = 0; k < S::N; k++) v[k] = stored<XT>(v[k] * rstd * w[k]);
+  if (a.y != nullptr) sp.template put<NT>(static_cast<XT*>(a.y) + at, v);
+
+  const size_t row = blockIdx.x;
   if constexpr (FMT == 2 || FMT == 4) {
     uint8_t* const codes = a.codes + row * (FMT == 2 ? cols : cols / 2);
 #pragma unroll
     for (int i = 0; i < CH; i++)
-      encode_mx<FMT>(v[i], tid + nt * i, codes, a.scales + row * (cols / 32), 8 * (tid + nt * i) < cols);
+      encode_mx<FMT>(v + 8 * i, sp.piece(i), codes, a.scales + row * (cols / 32), sp.has(8 * i));
   }
   if constexpr (FMT == 1) {
     float gs = a.gs_val;
@@ -153,180 +143,213 @@ __global__ __launch_bounds__(1024) void k_norm_forward(NormArgs a) {
     if (a.gs_row) {
       float A = 0.0f;
 #pragma unroll
-      for (int i = 0; i < CH; i++) A = fmaxf(A, 8 * (tid + nt * i) < cols ? amax8(v[i]) : 0.0f);
+      for (int i = 0; i < CH; i++) A = fmaxf(A, sp.has(8 * i) ? amax8(v + 8 * i) : 0.0f);
       A = group_amax(A, red[1]);
       zero_row = A == 0.0f;
       gs = nvfp4_gs(A);
     }
-    if (tid == 0) a.row_gs[row] = gs;
+    if (threadIdx.x == 0) a.row_gs[row] = gs;
 #pragma unroll
     for (int i = 0; i < CH; i++)
-      encode_nv(v[i], tid + nt * i, gs, zero_row, a.codes + row * (cols / 2), a.scales + row * (cols / 16),
-                8 * (tid + nt * i) < cols);
+      encode_nv(v + 8 * i, sp.piece(i), gs, zero_row, a.codes + row * (cols / 2), a.scales + row * (cols / 16),
+                sp.has(8 * i));
   }
 }
 
 // Rows blockIdx, blockIdx + grid, ..; this workgroup's share of dw stays in
-// registers and goes to partial[blockIdx].
-template <typename XT, typename RT, bool VEC, int CH>
-__global__ __launch_bounds__(1024) void k_norm_backward(NormGradArgs a) {
+// registers and goes to partial[blockIdx].  AHEAD (up to 8 waves, which leave the
+// registers for it): the next row's loads go out before this row's stores,
+// behind which they would wait for them (memory operations complete in order):
+// 16384 x 4608 with an fp32 stream 241 us instead of 273.
+template <typename XT, typename RT, bool FULL, int CH, int TB, bool NT>
+__global__ __launch_bounds__(TB) void k_norm_backward(NormGradArgs a) {
   __shared__ float red[2][16];
-  const int tid = threadIdx.x, nt = blockDim.x, cols = a.cols;
-  float w[CH][8], acc[CH][8];
+  typedef Span<FULL, CH> S;
+  const S sp(a.cols, blockDim.x);
+  const XT* const dy = static_cast<const XT*>(a.dy);
+  const RT* const res = static_cast<const RT*>(a.res);
+  const RT* const next = static_cast<const RT*>(a.d_res_out);
+  constexpr bool AHEAD = TB <= 512;
+  float w[S::N], acc[S::N];
+  auto fetch_weight = [&]() {
+    typename S::template Raw<float> rw;
+    sp.load(rw, a.weight);
+    sp.get(rw, w);
+  };
+  if (AHEAD) fetch_weight();
 #pragma unroll
-  for (int i = 0; i < CH; i++) {
-    Raw8<float> rw;
-    load_raw8<VEC>(rw, a.weight, tid + nt * i, cols);
-    rw.get(w[i]);
-#pragma unroll
-    for (int e = 0; e < 8; e++) acc[i][e] = 0.0f;
-  }
+  for (int k = 0; k < S::N; k++) acc[k] = 0.0f;
+
+  typename S::template Raw<XT> rdy;
+  typename S::template Raw<RT> rs, rn;
+  float rstd_raw;
+  auto fetch = [&](int t) {
+    const size_t at = (size_t)t * a.cols;
+    rstd_raw = a.rstd[t];
+    sp.template load<NT>(rdy, dy + at);
+    sp.template load<NT>(rs, res + at);
+    if (next != nullptr) sp.template load<NT>(rn, next + at);
+  };
+  if (AHEAD) fetch(blockIdx.x);
   int turn = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-    const size_t at = (size_t)t * cols;
-    Raw8<XT> rdy[CH];
-    Raw8<RT> rs[CH], rn[CH];
-#pragma unroll
-    for (int i = 0; i < CH; i++) {
-      load_raw8<VEC>(rdy[i], static_cast<const XT*>(a.dy) + at, tid + nt * i, cols);
-      load_raw8<VEC>(rs[i], static_cast<const RT*>(a.res) + at, tid + nt * i, cols);
+    const size_t at = (size_t)t * a.cols;
+    if (!AHEAD) {
+      fetch(t);
+      fetch_weight();
     }
-    if (a.d_res_out != nullptr) {
+    const float rstd = rstd_raw;
+    float n[S::N], g[S::N], d[S::N], dot = 0.0f;
+    sp.get(rdy, g);
+    sp.get(rs, n);
 #pragma unroll
-      for (int i = 0; i < CH; i++) load_raw8<VEC>(rn[i], static_cast<const RT*>(a.d_res_out) + at, tid + nt * i, cols);
+    for (int k = 0; k < S::N; k++) {
+      n[k] = sp.has(k) ? n[k] * rstd : 0.0f;
+      const float gn = sp.has(k) ? g[k] * n[k] : 0.0f;
+      acc[k] += gn;
+      dot = fmaf(gn, w[k], dot);
     }
-    const float rstd = a.rstd[t];
-    float n[CH][8], g[CH][8], dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < CH; i++) {
-      rdy[i].get(g[i]);
-      rs[i].get(n[i]);
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const bool in = in_row<VEC>(tid + nt * i, e, cols);
-        n[i][e] = in ? n[i][e] * rstd : 0.0f;
-        const float gn = in ? g[i][e] * n[i][e] : 0.0f;
-        acc[i][e] += gn;
-        dot = fmaf(gn, w[i][e], dot);
-      }
+    if (AHEAD) {
+      if (next != nullptr) sp.get(rn, d);
+      fetch(min(t + (int)gridDim.x, a.T - 1));
     }
-    dot = group_total(dot, red[turn]) / (float)cols;
+    dot = group_total(dot, red[turn]) / (float)a.cols;
 #pragma unroll
-    for (int i = 0; i < CH; i++) {
-      float d[8];
-#pragma unroll
-      for (int e = 0; e < 8; e++) d[e] = rstd * (g[i][e] * w[i][e] - n[i][e] * dot);
-      if (a.d_res_out != nullptr) {
-        float u[8];
-        rn[i].get(u);
-#pragma unroll
-        for (int e = 0; e < 8; e++) d[e] += u[e];
-      }
-      store8<VEC>(static_cast<RT*>(a.d_res) + at, tid + nt * i, cols, d);
-      if (a.dx != nullptr) store8<VEC>(static_cast<XT*>(a.dx) + at, tid + nt * i, cols, d);
+    for (int k = 0; k < S::N; k++) {
+      if (!AHEAD && k == 0 && next != nullptr) sp.get(rn, d);
+      const float v = rstd * (g[k] * w[k] - n[k] * dot);
+      d[k] = next != nullptr ? v + d[k] : v;
     }
+    sp.template put<NT>(static_cast<RT*>(a.d_res) + at, d);
+    if (a.dx != nullptr) sp.template put<NT>(static_cast<XT*>(a.dx) + at, d);
   }
   if (a.partial != nullptr) {
-#pragma unroll
-    for (int i = 0; i < CH; i++) store8<VEC>(a.partial + (size_t)blockIdx.x * cols, tid + nt * i, cols, acc[i]);
+    float* const row = a.partial + (size_t)blockIdx.x * a.pitch;
+    sp.put(row, acc);
   }
 }
 
-// dw: the partial rows added in order, 32 columns a workgroup, 8 runs of rows.
-__global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ partial, int n, int cols,
-                                                 float* __restrict__ dw) {
-  __shared__ float part[8][32];
-  const int c = threadIdx.x & 31, run = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-  const int lo = (long)run * n / 8, hi = (long)(run + 1) * n / 8;
-  float s = 0.0f;
-  for (int i = lo; i < hi; i++) s += col < cols ? partial[(size_t)i * cols + col] : 0.0f;
+// dw: the partial rows added up, 32 columns a workgroup; run r of 128 takes rows
+// r, r + 128, .., then 8 threads a column 16 runs each, then one those 8.
+__global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ partial, int n, int cols, int pitch,
+                                                  float* __restrict__ dw) {
+  __shared__ v4f part[128][8];
+  const int c = threadIdx.x & 7, run = threadIdx.x >> 3, col = blockIdx.x * 32 + 4 * c;
+  v4f s = v4f{0, 0, 0, 0};
+  if (col < pitch) {
+    const float* p = partial + col;
+    int i = run;
+    for (; i + 3 * 128 < n; i += 4 * 128) {
+      v4f v[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[j] = *reinterpret_cast<const v4f*>(p + (size_t)(i + 128 * j) * pitch);
+#pragma unroll
+      for (int j = 0; j < 4; j++) s += v[j];
+    }
+    for (; i < n; i += 128) s += *reinterpret_cast<const v4f*>(p + (size_t)i * pitch);
+  }
   part[run][c] = s;
   __syncthreads();
-  if (run == 0 && col < cols) {
+  if (run < 8)
+    for (int i = run + 8; i < 128; i += 8) s += part[i][c];
+  __syncthreads();
+  if (run < 8) part[run][c] = s;
+  __syncthreads();
+  if (run == 0) {
     for (int i = 1; i < 8; i++) s += part[i][c];
-    dw[col] = s;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (col + e < cols) dw[col + e] = s[e];
   }
 }
 
 namespace {
 
-constexpr int kRowPieces = 4;   // of 8 elements a lane; 8 in the widest rows
-
-// Pieces a lane has in a workgroup of row_waves.
-int row_pieces(int cols, int waves) {
-  const int n = ceil_div(ceil_div(cols, 8), 64L * waves);
-  return n > 4 ? 8 : n;
+template <typename XT, typename RT, int FMT, bool FULL, bool NT>
+void forward_ch(const NormArgs& a, hipStream_t s) {
+  const int waves = row_waves(a.cols, 4);
+  MOE_ROW_PIECES(row_pieces(a.cols, waves),
+                 hipLaunchKernelGGL((k_norm_forward<XT, RT, FMT, FULL, CH, NT>), dim3(a.T), dim3(64 * waves), 0, s, a))
+}
+template <typename XT, typename RT, bool NT>
+void forward_fmt(const NormArgs& a, bool full, hipStream_t s) {
+  if (a.fmt == 1) forward_ch<XT, RT, 1, true, NT>(a, s);
+  else if (a.fmt == 2) forward_ch<XT, RT, 2, true, NT>(a, s);
+  else if (a.fmt == 4) forward_ch<XT, RT, 4, true, NT>(a, s);
+  else if (full) forward_ch<XT, RT, 0, true, NT>(a, s);
+  else forward_ch<XT, RT, 0, false, NT>(a, s);
+}
+template <typename XT, typename RT>
+void forward_nt(const NormArgs& a, bool full, hipStream_t s) {
+  const size_t bytes = (size_t)a.T * a.cols * (sizeof(XT) + sizeof(RT));
+  if (bytes > kStreamBytes) forward_fmt<XT, RT, true>(a, full, s);
+  else forward_fmt<XT, RT, false>(a, full, s);
 }
 
-template <typename XT, typename RT, int FMT, bool VEC>
-void forward_ch(const NormArgs& a, hipStream_t s) {
-  const int waves = row_waves(a.cols, kRowPieces);
-  const dim3 grid(a.T), block(64 * waves);
-  switch (row_pieces(a.cols, waves)) {
-    case 1: hipLaunchKernelGGL((k_norm_forward<XT, RT, FMT, VEC, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((k_norm_forward<XT, RT, FMT, VEC, 2>), grid, block, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((k_norm_forward<XT, RT, FMT, VEC, 3>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((k_norm_forward<XT, RT, FMT, VEC, 4>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_norm_forward<XT, RT, FMT, VEC, 8>), grid, block, 0, s, a); break;
+// Waves of a row's workgroup in the gradient, and workgroups.
+int gradient_waves(int cols) { return row_waves(cols, row_waves(cols, 3) <= 8 ? 3 : 2); }
+// More of them for short rows, which need more in flight, as long as their partial
+// sums stay small: 65536 x 256 took 126 us with 512, 67 with 4096.
+int gradient_groups(int T, int cols) {
+  const int n = (256 * 4608) / cols;
+  const int g = n < 512 ? 512 : n < 4096 ? n : 4096;
+  return T < g ? T : g;
+}
+int partial_pitch(int cols) { return (int)align_up(cols, 8); }
+
+template <typename XT, typename RT, bool FULL, bool NT>
+void backward_ch(const NormGradArgs& a, int grid, hipStream_t s) {
+  const int waves = gradient_waves(a.cols);
+  if (waves <= 4) {
+    MOE_ROW_PIECES(row_pieces(a.cols, waves),
+                   hipLaunchKernelGGL((k_norm_backward<XT, RT, FULL, CH, 256, NT>), dim3(grid), dim3(64 * waves), 0, s, a))
+  } else if (waves <= 8) {
+    MOE_ROW_PIECES(row_pieces(a.cols, waves),
+                   hipLaunchKernelGGL((k_norm_backward<XT, RT, FULL, CH, 512, NT>), dim3(grid), dim3(64 * waves), 0, s, a))
+  } else {
+    MOE_ROW_PIECES(row_pieces(a.cols, waves),
+                   hipLaunchKernelGGL((k_norm_backward<XT, RT, FULL, CH, 1024, NT>), dim3(grid), dim3(64 * waves), 0, s, a))
   }
 }
 template <typename XT, typename RT>
-void forward_fmt(const NormArgs& a, bool vec, hipStream_t s) {
-  if (a.fmt == 1) forward_ch<XT, RT, 1, true>(a, s);
-  else if (a.fmt == 2) forward_ch<XT, RT, 2, true>(a, s);
-  else if (a.fmt == 4) forward_ch<XT, RT, 4, true>(a, s);
-  else if (vec) forward_ch<XT, RT, 0, true>(a, s);
-  else forward_ch<XT, RT, 0, false>(a, s);
+void backward_full(const NormGradArgs& a, bool full, int grid, hipStream_t s) {
+  const bool nt = (size_t)a.T * a.cols * (sizeof(XT) + sizeof(RT)) > kStreamBytes;
+  if (full && nt) backward_ch<XT, RT, true, true>(a, grid, s);
+  else if (full) backward_ch<XT, RT, true, false>(a, grid, s);
+  else if (nt) backward_ch<XT, RT, false, true>(a, grid, s);
+  else backward_ch<XT, RT, false, false>(a, grid, s);
 }
-
-template <typename XT, typename RT, bool VEC>
-void backward_ch(const NormGradArgs& a, int grid, hipStream_t s) {
-  const int waves = row_waves(a.cols, kRowPieces);
-  const dim3 block(64 * waves);
-  switch (row_pieces(a.cols, waves)) {
-    case 1: hipLaunchKernelGGL((k_norm_backward<XT, RT, VEC, 1>), dim3(grid), block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((k_norm_backward<XT, RT, VEC, 2>), dim3(grid), block, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((k_norm_backward<XT, RT, VEC, 3>), dim3(grid), block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((k_norm_backward<XT, RT, VEC, 4>), dim3(grid), block, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_norm_backward<XT, RT, VEC, 8>), dim3(grid), block, 0, s, a); break;
-  }
-}
-
-// Workgroups of the gradient of T rows.
-int gradient_groups(int T) { return T < 1024 ? T : 1024; }
 
 }  // namespace
 
-size_t norm_ws_bytes(int T, int cols) { return align_up((size_t)gradient_groups(T) * cols * 4, 256); }
+size_t norm_ws_bytes(int T, int cols) {
+  return align_up((size_t)gradient_groups(T, cols) * partial_pitch(cols) * 4, 256);
+}
 
 int launch_norm_forward(const NormArgs& a, hipStream_t stream) {
   if (a.T <= 0) return 0;
-  const bool vec = a.cols % 8 == 0 && aligned16(a.x) && aligned16(a.res) && aligned16(a.res_out) && aligned16(a.y) &&
-                   aligned16(a.weight);
-  if (a.dtype == 0 && a.res_dtype == 0) forward_fmt<uint16_t, uint16_t>(a, vec, stream);
-  else if (a.dtype == 0) forward_fmt<uint16_t, float>(a, vec, stream);
-  else forward_fmt<float, float>(a, vec, stream);
+  const bool full = a.cols % 8 == 0 && aligned16(a.x) && aligned16(a.res) && aligned16(a.res_out) && aligned16(a.y) &&
+                    aligned16(a.weight);
+  if (a.dtype == 0 && a.res_dtype == 0) forward_nt<uint16_t, uint16_t>(a, full, stream);
+  else if (a.dtype == 0) forward_nt<uint16_t, float>(a, full, stream);
+  else forward_nt<float, float>(a, full, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_norm_backward(NormGradArgs a, float* d_weight, void* ws, hipStream_t stream) {
-  const bool vec = a.cols % 8 == 0 && aligned16(a.dy) && aligned16(a.res) && aligned16(a.d_res_out) &&
-                   aligned16(a.weight) && aligned16(a.d_res) && aligned16(a.dx);
-  const int grid = gradient_groups(a.T);
+  const bool full = a.cols % 8 == 0 && aligned16(a.dy) && aligned16(a.res) && aligned16(a.d_res_out) &&
+                    aligned16(a.weight) && aligned16(a.d_res) && aligned16(a.dx);
+  const int grid = gradient_groups(a.T, a.cols);
   a.partial = d_weight == nullptr ? nullptr : static_cast<float*>(ws);
+  a.pitch = partial_pitch(a.cols);
   if (a.T > 0) {
-#define MOE_NORM_BACK(XT, RT)                            \
-  do {                                                   \
-    if (vec) backward_ch<XT, RT, true>(a, grid, stream); \
-    else backward_ch<XT, RT, false>(a, grid, stream);    \
-  } while (0)
-    if (a.dtype == 0 && a.res_dtype == 0) MOE_NORM_BACK(uint16_t, uint16_t);
-    else if (a.dtype == 0) MOE_NORM_BACK(uint16_t, float);
-    else MOE_NORM_BACK(float, float);
-#undef MOE_NORM_BACK
+    if (a.dtype == 0 && a.res_dtype == 0) backward_full<uint16_t, uint16_t>(a, full, grid, stream);
+    else if (a.dtype == 0) backward_full<uint16_t, float>(a, full, grid, stream);
+    else backward_full<float, float>(a, full, grid, stream);
   }
   if (d_weight != nullptr)
-    hipLaunchKernelGGL(k_norm_dw, dim3(ceil_div(a.cols, 32)), dim3(256), 0, stream, a.partial, grid, a.cols, d_weight);
+    hipLaunchKernelGGL(k_norm_dw, dim3(ceil_div(a.cols, 32)), dim3(1024), 0, stream, a.partial, grid, a.cols, a.pitch,
+                       d_weight);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -97,7 +97,8 @@ struct NormGradArgs {
   const float* rstd;
   void* d_res;
   void* dx;                 // nullable
-  float* partial;           // set by the launcher
+  float* partial;           // [workgroups][pitch], set by the launcher
+  int pitch;
 };
 size_t norm_ws_bytes(int T, int cols);
 int launch_norm_forward(const NormArgs& a, hipStream_t stream);

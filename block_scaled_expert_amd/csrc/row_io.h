@@ -83,83 +83,156 @@ struct Raw8<float> {
   }
 };
 
-template <bool NT, typename T>
-__device__ inline T get_nt(const T* p) {
-  if constexpr (NT) return __builtin_nontemporal_load(p);
-  else return *p;
-}
-template <bool NT, typename T>
-__device__ inline void put_nt(T* p, T v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
+// 16 bytes at an address that is a multiple of 16, or of the element's size alone.
+template <typename T, bool FULL>
+struct Wide;
+template <>
+struct Wide<uint16_t, true> {
+  typedef v4u V;
+};
+template <>
+struct Wide<uint16_t, false> {
+  typedef v4u V __attribute__((aligned(2)));
+};
+template <>
+struct Wide<float, true> {
+  typedef v4f V;
+};
+template <>
+struct Wide<float, false> {
+  typedef v4f V __attribute__((aligned(4)));
+};
 
-// Elements 8 c .. 8 c + 7 of a row of `cols`.  VEC: 16-byte accesses (cols a
-// multiple of 8, rows 16-byte aligned), else one element at a time.  Loads of
-// chunks or elements past the row read its last ones, so none sits under a
-// branch; what they return is not used.
-template <bool VEC, bool NT = false>
-__device__ inline void load_raw8(Raw8<uint16_t>& r, const uint16_t* row, int c, int cols) {
-  if constexpr (VEC) {
-    r.w = get_nt<NT>(reinterpret_cast<const v4u*>(row) + min(c, cols / 8 - 1));
+// NT: the hint for bytes that are used once (see kStreamBytes).
+template <bool FULL, bool NT>
+__device__ inline void load8(Raw8<uint16_t>& r, const uint16_t* p) {
+  const auto* q = reinterpret_cast<const typename Wide<uint16_t, FULL>::V*>(p);
+  r.w = NT ? __builtin_nontemporal_load(q) : *q;
+}
+template <bool FULL, bool NT>
+__device__ inline void load8(Raw8<float>& r, const float* p) {
+  const auto* q = reinterpret_cast<const typename Wide<float, FULL>::V*>(p);
+  r.a = NT ? __builtin_nontemporal_load(q) : *q;
+  r.b = NT ? __builtin_nontemporal_load(q + 1) : q[1];
+}
+template <bool FULL, bool NT>
+__device__ inline void store8(uint16_t* p, const Raw8<uint16_t>& r) {
+  auto* q = reinterpret_cast<typename Wide<uint16_t, FULL>::V*>(p);
+  if constexpr (NT) __builtin_nontemporal_store(r.w, q);
+  else *q = r.w;
+}
+template <bool FULL, bool NT>
+__device__ inline void store8(float* p, const Raw8<float>& r) {
+  auto* q = reinterpret_cast<typename Wide<float, FULL>::V*>(p);
+  if constexpr (NT) {
+    __builtin_nontemporal_store(r.a, q);
+    __builtin_nontemporal_store(r.b, q + 1);
   } else {
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      r.w[j] = (uint32_t)row[min(8 * c + 2 * j, cols - 1)] | (uint32_t)row[min(8 * c + 2 * j + 1, cols - 1)] << 16;
+    q[0] = r.a;
+    q[1] = r.b;
   }
 }
-template <bool VEC, bool NT = false>
-__device__ inline void load_raw8(Raw8<float>& r, const float* row, int c, int cols) {
-  if constexpr (VEC) {
-    const v4f* p = reinterpret_cast<const v4f*>(row) + 2 * min(c, cols / 8 - 1);
-    r.a = get_nt<NT>(p);
-    r.b = get_nt<NT>(p + 1);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      r.a[j] = row[min(8 * c + j, cols - 1)];
-      r.b[j] = row[min(8 * c + 4 + j, cols - 1)];
-    }
-  }
+__device__ inline void set(Raw8<uint16_t>& r, const float* v) {
+  r.w = v4u{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
 }
-// Element e of chunk c lies in the row.
-template <bool VEC>
-__device__ inline bool in_row(int c, int e, int cols) {
-  return VEC ? 8 * c < cols : 8 * c + e < cols;
+__device__ inline void set(Raw8<float>& r, const float* v) {
+  r.a = v4f{v[0], v[1], v[2], v[3]};
+  r.b = v4f{v[4], v[5], v[6], v[7]};
 }
-template <bool VEC, bool NT = false>
-__device__ inline void store8(uint16_t* row, int c, int cols, const float (&v)[8]) {
-  if constexpr (VEC) {
-    if (8 * c < cols)
-      put_nt<NT>(reinterpret_cast<v4u*>(row) + c,
-                 v4u{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])});
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (8 * c + j < cols) row[8 * c + j] = bf16_bits(v[j]);
-  }
-}
-template <bool VEC, bool NT = false>
-__device__ inline void store8(float* row, int c, int cols, const float (&v)[8]) {
-  if constexpr (VEC) {
-    if (8 * c < cols) {
-      v4f* p = reinterpret_cast<v4f*>(row) + 2 * c;
-      put_nt<NT>(p, v4f{v[0], v[1], v[2], v[3]});
-      put_nt<NT>(p + 1, v4f{v[4], v[5], v[6], v[7]});
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (8 * c + j < cols) row[8 * c + j] = v[j];
-  }
-}
+__device__ inline float widen1(uint16_t h) { return bf16_to_f32(h); }
+__device__ inline float widen1(float f) { return f; }
+__device__ inline void set1(uint16_t& h, float f) { h = bf16_bits(f); }
+__device__ inline void set1(float& h, float f) { h = f; }
 
-// Waves of a workgroup that takes a row in pieces of 8 elements a lane, `per`
-// pieces a lane at most: the fewest, up to 16.
+// The part of a row of `cols` elements that a thread holds: pieces of 8
+// elements at thread, thread + threads, .. (CH of them, from piece `from` on)
+// and, unless FULL, one of the cols % 8 elements behind the last whole piece.
+// FULL: cols is a multiple of 8 and rows are 16-byte aligned; else they need only
+// be aligned to their elements.  Loads past the row read its last piece or
+// element, so that none sits under a branch; what they return is finite where the
+// row is and not used.
+template <bool FULL, int CH>
+struct Span {
+  static constexpr int N = 8 * CH + (FULL ? 0 : 1);
+  template <typename T>
+  struct Raw {
+    Raw8<T> c[CH];
+    T t;
+  };
+  int c0, step, n8, rem, cols;
+
+  __device__ Span(int cols_, int threads, int from = 0)
+      : c0(from + (int)threadIdx.x), step(threads), n8(cols_ / 8), rem(FULL || from > 0 ? 0 : cols_ % 8), cols(cols_) {}
+  // Whether element k of the thread's N lies in the row.
+  __device__ bool has(int k) const { return k < 8 * CH ? c0 + step * (k / 8) < n8 : (int)threadIdx.x < rem; }
+  __device__ int piece(int i) const { return c0 + step * i; }
+
+  template <bool NT = false, typename T>
+  __device__ void load(Raw<T>& r, const T* row) const {
+    if (FULL || n8 > 0) {
+#pragma unroll
+      for (int i = 0; i < CH; i++) load8<FULL, NT>(r.c[i], row + 8 * min(piece(i), n8 - 1));
+    } else {
+      const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < CH; i++) set(r.c[i], zero);
+    }
+    if constexpr (!FULL) r.t = row[min(8 * n8 + (int)threadIdx.x, cols - 1)];
+  }
+  template <typename T>
+  __device__ void get(const Raw<T>& r, float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      float u[8];
+      r.c[i].get(u);
+#pragma unroll
+      for (int e = 0; e < 8; e++) v[8 * i + e] = u[e];
+    }
+    if constexpr (!FULL) v[8 * CH] = widen1(r.t);
+  }
+  template <typename T>
+  __device__ void set_raw(Raw<T>& r, const float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < CH; i++) set(r.c[i], v + 8 * i);
+    if constexpr (!FULL) set1(r.t, v[8 * CH]);
+  }
+  template <bool NT = false, typename T>
+  __device__ void store(T* row, const Raw<T>& r) const {
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+      if (piece(i) < n8) store8<FULL, NT>(row + 8 * piece(i), r.c[i]);
+    if constexpr (!FULL)
+      if ((int)threadIdx.x < rem) row[8 * n8 + (int)threadIdx.x] = r.t;
+  }
+  template <bool NT = false, typename T>
+  __device__ void put(T* row, const float (&v)[N]) const {
+    Raw<T> r;
+    set_raw(r, v);
+    store<NT>(row, r);
+  }
+};
+
+// Waves of a workgroup that holds a row in pieces of 8, at most `per` a thread:
+// the fewest, up to 16 (at least 8 threads for the elements behind the pieces).
 inline int row_waves(int cols, int per) {
-  const int n = ceil_div(ceil_div(cols, 8), 64L * per);
-  return n < 16 ? n : 16;
+  const int n = ceil_div(cols / 8, 64L * per);
+  return n < 1 ? 1 : n < 16 ? n : 16;
+}
+// Pieces of a thread then, as the kernels are built for them.
+inline int row_pieces(int cols, int waves) {
+  const int n = ceil_div(cols / 8, 64L * waves);
+  return n < 1 ? 1 : n > 4 ? 8 : n;
 }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// CALL with the constant CH = n, of 1, 2, 3, 4 and 8.
+#define MOE_ROW_PIECES(n, CALL) \
+  switch (n) {                  \
+    case 1: { constexpr int CH = 1; CALL; } break; \
+    case 2: { constexpr int CH = 2; CALL; } break; \
+    case 3: { constexpr int CH = 3; CALL; } break; \
+    case 4: { constexpr int CH = 4; CALL; } break; \
+    default: { constexpr int CH = 8; CALL; } break; \
+  }
 
 }  // namespace moe

@@ -40,98 +40,112 @@ __device__ inline int next_slot(uint64_t& m) {
 
 }  // namespace
 
-// One chunk of 8 columns a thread; blockIdx.x token, blockIdx.y run of columns.
-template <typename T, bool VEC, bool NT>
-__global__ __launch_bounds__(256) void k_sort_rows(RowsArgs a) {
-  const int t = blockIdx.x, c = blockIdx.y * blockDim.x + threadIdx.x;
-  Raw8<T> r;
-  load_raw8<VEC>(r, static_cast<const T*>(a.token) + (size_t)t * a.cols, c, a.cols);
+// blockIdx.x token, blockIdx.y run of columns (one for many tokens).
+template <typename T, bool FULL, int CH, bool NT>
+__global__ __launch_bounds__(1024) void k_sort_rows(RowsArgs a) {
+  typedef Span<FULL, CH> S;
+  const int t = blockIdx.x;
+  const S sp(a.cols, blockDim.x, blockIdx.y * blockDim.x * CH);
+  typename S::template Raw<T> r;
+  sp.template load<NT>(r, static_cast<const T*>(a.token) + (size_t)t * a.cols);
   const Pairs p(a, t);
-  float v[8];
-  r.get(v);
-  for (uint64_t m = p.on; m != 0;) {
+  for (uint64_t m = p.on; m != 0;)
+    sp.template store<NT>(static_cast<T*>(a.rows_out) + (size_t)p.row(next_slot(m)) * a.cols, r);
+}
+
+// acc += the next n of the slots in m, whose loads go out together.
+template <int n, bool NT, typename YT, typename S>
+__device__ inline void add_slots(const RowsArgs& a, const S& sp, const Pairs& p, uint64_t& m, float (&acc)[S::N]) {
+  typename S::template Raw<YT> r[n];
+  float w[n];
+#pragma unroll
+  for (int i = 0; i < n; i++) {
     const int j = next_slot(m);
-    store8<VEC, NT>(static_cast<T*>(a.rows_out) + (size_t)p.row(j) * a.cols, c, a.cols, v);
+    w[i] = p.weight(j);
+    sp.template load<NT>(r[i], static_cast<const YT*>(a.rows_in) + (size_t)p.row(j) * a.cols);
+  }
+#pragma unroll
+  for (int i = 0; i < n; i++) {
+    float v[S::N];
+    sp.get(r[i], v);
+#pragma unroll
+    for (int k = 0; k < S::N; k++) acc[k] = fmaf(w[i], v[k], acc[k]);
   }
 }
 
-constexpr int kSlots = 4;   // rows in flight
-
-template <typename YT, typename OT, bool VEC, bool NT>
-__global__ __launch_bounds__(256) void k_combine_rows(RowsArgs a) {
-  const int t = blockIdx.x, c = blockIdx.y * blockDim.x + threadIdx.x;
+template <typename YT, typename OT, bool FULL, int CH, bool NT>
+__global__ __launch_bounds__(1024) void k_combine_rows(RowsArgs a) {
+  typedef Span<FULL, CH> S;
+  const int t = blockIdx.x;
+  const S sp(a.cols, blockDim.x, blockIdx.y * blockDim.x * CH);
   const Pairs p(a, t);
-  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (uint64_t m = p.on; m != 0;) {
-    Raw8<YT> r[kSlots];
-    float w[kSlots];
-    bool on[kSlots];
-    int j = 0;
+  float acc[S::N];
 #pragma unroll
-    for (int i = 0; i < kSlots; i++) {   // past the last slot: its row again, unused
-      on[i] = m != 0;
-      if (on[i]) j = next_slot(m);
-      w[i] = p.weight(j);
-      load_raw8<VEC, NT>(r[i], static_cast<const YT*>(a.rows_in) + (size_t)p.row(j) * a.cols, c, a.cols);
-    }
-#pragma unroll
-    for (int i = 0; i < kSlots; i++) {
-      float v[8];
-      r[i].get(v);
-#pragma unroll
-      for (int e = 0; e < 8; e++) acc[e] = on[i] ? fmaf(w[i], v[e], acc[e]) : acc[e];
-    }
-  }
-  store8<VEC>(static_cast<OT*>(a.token_out) + (size_t)t * a.cols, c, a.cols, acc);
+  for (int k = 0; k < S::N; k++) acc[k] = 0.0f;
+  uint64_t m = p.on;
+  int left = __builtin_popcountll(m);
+  for (; left >= 4; left -= 4) add_slots<4, NT, YT>(a, sp, p, m, acc);
+  if (left >= 2) add_slots<2, NT, YT>(a, sp, p, m, acc);
+  if (left & 1) add_slots<1, NT, YT>(a, sp, p, m, acc);
+  sp.put(static_cast<OT*>(a.token_out) + (size_t)t * a.cols, acc);
 }
 
-// One workgroup per token, whose d_out row stays in registers for all its slots.
-template <typename YT, typename OT, bool VEC, bool NT, int CH>
+// One workgroup per token, whose d_out row stays in registers for all its
+// slots.  The next slot's row is loaded before this slot's stores (memory
+// operations complete in order).
+template <typename YT, typename OT, bool FULL, int CH, bool NT>
 __global__ __launch_bounds__(1024) void k_combine_rows_backward(RowsArgs a) {
   __shared__ float part[32][16];
-  const int t = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, waves = nt >> 6;
-  float d[CH][8];
-  {
-    Raw8<OT> r[CH];
-#pragma unroll
-    for (int i = 0; i < CH; i++)
-      load_raw8<VEC>(r[i], static_cast<const OT*>(a.token) + (size_t)t * a.cols, tid + nt * i, a.cols);
-#pragma unroll
-    for (int i = 0; i < CH; i++) {
-      r[i].get(d[i]);
-#pragma unroll
-      for (int e = 0; e < 8; e++) d[i][e] = in_row<VEC>(tid + nt * i, e, a.cols) ? d[i][e] : 0.0f;
-    }
-  }
+  typedef Span<FULL, CH> S;
+  const int t = blockIdx.x, tid = threadIdx.x, waves = blockDim.x >> 6;
+  const S sp(a.cols, blockDim.x);
+  typename S::template Raw<OT> rd;
+  sp.template load<NT>(rd, static_cast<const OT*>(a.token) + (size_t)t * a.cols);
   const Pairs p(a, t);
-  for (uint64_t m = p.on; m != 0;) {
-    const int j = next_slot(m);
-    const size_t at = (size_t)p.row(j) * a.cols;
-    const float w = p.weight(j);
+  typedef typename S::template Raw<YT> Row;
+  uint64_t m = p.on;
+  int j = 0;
+  auto fetch = [&](Row& r) {
+    j = next_slot(m);
+    if (a.d_w != nullptr) sp.template load<NT>(r, static_cast<const YT*>(a.rows_in) + (size_t)p.row(j) * a.cols);
+  };
+  float d[S::N];
+  auto slot = [&](const Row& r, int s) {
     if (a.d_w != nullptr) {
-      Raw8<YT> r[CH];
+      float y[S::N], dot = 0.0f;
+      sp.get(r, y);
 #pragma unroll
-      for (int i = 0; i < CH; i++)
-        load_raw8<VEC, NT>(r[i], static_cast<const YT*>(a.rows_in) + at, tid + nt * i, a.cols);
-      float dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < CH; i++) {
-        float y[8];
-        r[i].get(y);
-#pragma unroll
-        for (int e = 0; e < 8; e++) dot = in_row<VEC>(tid + nt * i, e, a.cols) ? fmaf(d[i][e], y[e], dot) : dot;
-      }
+      for (int k = 0; k < S::N; k++) dot = sp.has(k) ? fmaf(d[k], y[k], dot) : dot;
       dot = wave_total(dot);
-      if ((tid & 63) == 0) part[j][tid >> 6] = dot;
+      if ((tid & 63) == 0) part[s][tid >> 6] = dot;
     }
     if (a.rows_out != nullptr) {
+      const float w = p.weight(s);
+      float g[S::N];
 #pragma unroll
-      for (int i = 0; i < CH; i++) {
-        float g[8];
-#pragma unroll
-        for (int e = 0; e < 8; e++) g[e] = w * d[i][e];
-        store8<VEC, NT>(static_cast<YT*>(a.rows_out) + at, tid + nt * i, a.cols, g);
+      for (int k = 0; k < S::N; k++) g[k] = w * d[k];
+      sp.template put<NT>(static_cast<YT*>(a.rows_out) + (size_t)p.row(s) * a.cols, g);
+    }
+  };
+  if (m != 0) {
+    Row r0, r1;
+    fetch(r0);
+    sp.get(rd, d);
+    for (;;) {
+      int s = j;
+      if (m == 0) {
+        slot(r0, s);
+        break;
       }
+      fetch(r1);
+      slot(r0, s);
+      s = j;
+      if (m == 0) {
+        slot(r1, s);
+        break;
+      }
+      fetch(r0);
+      slot(r1, s);
     }
   }
   if (a.d_w == nullptr) return;
@@ -146,34 +160,32 @@ __global__ __launch_bounds__(1024) void k_combine_rows_backward(RowsArgs a) {
 
 namespace {
 
-// Waves of a workgroup whose threads take one chunk of 8 columns each: those
-// that leave the fewest idle over the runs of a row.
-int column_waves(int cols) {
-  const int n = ceil_div(ceil_div(cols, 8), 64);
-  int best = 4;
-  for (int w = 3; w >= 1; w--)
-    if (ceil_div(n, w) * w < ceil_div(n, best) * best) best = w;
-  return best;
-}
-dim3 column_grid(const RowsArgs& a, int waves) {
-  return dim3(a.T, ceil_div(ceil_div(a.cols, 8), 64L * waves));
-}
-
-template <typename YT, typename OT, bool VEC, bool NT>
-void backward_ch(const RowsArgs& a, hipStream_t s) {
-  const int waves = row_waves(a.cols, 4), per = ceil_div(ceil_div(a.cols, 8), 64L * waves);
-  const dim3 grid(a.T), block(64 * waves);
-  switch (per) {
-    case 1: hipLaunchKernelGGL((k_combine_rows_backward<YT, OT, VEC, NT, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((k_combine_rows_backward<YT, OT, VEC, NT, 2>), grid, block, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((k_combine_rows_backward<YT, OT, VEC, NT, 3>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((k_combine_rows_backward<YT, OT, VEC, NT, 4>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((k_combine_rows_backward<YT, OT, VEC, NT, 8>), grid, block, 0, s, a); break;
+// Workgroups of a call that has a row's columns to itself: a whole row each for
+// many tokens, so that positions are fetched once a row; for few tokens a run of
+// 8 columns a thread, so that there are more of them.
+constexpr int kManyTokens = 1024;
+struct Shape {
+  int waves, pieces, runs;
+};
+Shape shape_of(const RowsArgs& a) {
+  Shape s;
+  const int n = ceil_div(a.cols / 8, 64);           // waves at one piece a thread
+  if (a.T >= kManyTokens) {
+    s.waves = row_waves(a.cols, 4);
+    s.pieces = row_pieces(a.cols, s.waves);
+    s.runs = 1;
+    return s;
   }
+  s.waves = 4;                                      // the number that leaves the fewest idle
+  for (int w = 3; w >= 1; w--)
+    if (ceil_div(n, w) * w < ceil_div(n, s.waves) * s.waves) s.waves = w;
+  s.pieces = 1;
+  s.runs = n > 0 ? ceil_div(n, s.waves) : 1;
+  return s;
 }
 
 // Bytes of the expert rows of a call.
-size_t row_bytes(const RowsArgs& a, int dtype) { return (size_t)a.M * a.cols * (dtype == 0 ? 2 : 4); }
+size_t row_bytes(const RowsArgs& a) { return (size_t)a.M * a.cols * (a.row_dtype == 0 ? 2 : 4); }
 
 }  // namespace
 
@@ -200,29 +212,31 @@ size_t row_bytes(const RowsArgs& a, int dtype) { return (size_t)a.M * a.cols * (
 
 int launch_sort_rows(const RowsArgs& a, hipStream_t s) {
   if (a.T <= 0) return 0;
-  const int waves = column_waves(a.cols);
-  const bool vec = a.cols % 8 == 0 && aligned16(a.token) && aligned16(a.rows_out);
-  const bool nt = row_bytes(a, a.row_dtype) > kStreamBytes;
-  MOE_ROWS_TYPE(a.row_dtype, T, MOE_ROWS_BOOL(vec, VEC, MOE_ROWS_BOOL(nt, NT, hipLaunchKernelGGL((k_sort_rows<T, VEC, NT>), column_grid(a, waves), dim3(64 * waves), 0, s, a))));
+  const Shape h = shape_of(a);
+  const bool full = a.cols % 8 == 0 && aligned16(a.token) && aligned16(a.rows_out), nt = row_bytes(a) > kStreamBytes;
+  MOE_ROWS_TYPE(a.row_dtype, T, MOE_ROWS_BOOL(full, FULL, MOE_ROWS_BOOL(nt, NT, MOE_ROW_PIECES(h.pieces,
+      hipLaunchKernelGGL((k_sort_rows<T, FULL, CH, NT>), dim3(a.T, h.runs), dim3(64 * h.waves), 0, s, a)))));
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_combine_rows(const RowsArgs& a, hipStream_t s) {
   if (a.T <= 0) return 0;
-  const int waves = column_waves(a.cols);
-  const bool vec = a.cols % 8 == 0 && aligned16(a.token_out) && aligned16(a.rows_in);
-  const bool nt = row_bytes(a, a.row_dtype) > kStreamBytes;
-  MOE_ROWS_TYPE(a.row_dtype, YT, MOE_ROWS_TYPE(a.token_dtype, OT, MOE_ROWS_BOOL(vec, VEC, MOE_ROWS_BOOL(nt, NT,
-      hipLaunchKernelGGL((k_combine_rows<YT, OT, VEC, NT>), column_grid(a, waves), dim3(64 * waves), 0, s, a)))));
+  const Shape h = shape_of(a);
+  const bool full = a.cols % 8 == 0 && aligned16(a.token_out) && aligned16(a.rows_in), nt = row_bytes(a) > kStreamBytes;
+  MOE_ROWS_TYPE(a.row_dtype, YT, MOE_ROWS_TYPE(a.token_dtype, OT, MOE_ROWS_BOOL(full, FULL, MOE_ROWS_BOOL(nt, NT,
+      MOE_ROW_PIECES(h.pieces, hipLaunchKernelGGL((k_combine_rows<YT, OT, FULL, CH, NT>), dim3(a.T, h.runs),
+                                                  dim3(64 * h.waves), 0, s, a))))));
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_combine_rows_backward(const RowsArgs& a, hipStream_t s) {
   if (a.T <= 0) return 0;
-  const bool vec = a.cols % 8 == 0 && aligned16(a.token) && aligned16(a.rows_in) && aligned16(a.rows_out);
-  const bool nt = row_bytes(a, a.row_dtype) > kStreamBytes;
-  MOE_ROWS_TYPE(a.row_dtype, YT, MOE_ROWS_TYPE(a.token_dtype, OT, MOE_ROWS_BOOL(vec, VEC, MOE_ROWS_BOOL(nt, NT,
-      (backward_ch<YT, OT, VEC, NT>(a, s))))));
+  const int waves = row_waves(a.cols, 4);
+  const bool full = a.cols % 8 == 0 && aligned16(a.token) && aligned16(a.rows_in) && aligned16(a.rows_out);
+  const bool nt = row_bytes(a) > kStreamBytes;
+  MOE_ROWS_TYPE(a.row_dtype, YT, MOE_ROWS_TYPE(a.token_dtype, OT, MOE_ROWS_BOOL(full, FULL, MOE_ROWS_BOOL(nt, NT,
+      MOE_ROW_PIECES(row_pieces(a.cols, waves), hipLaunchKernelGGL((k_combine_rows_backward<YT, OT, FULL, CH, NT>),
+                                                                   dim3(a.T), dim3(64 * waves), 0, s, a))))));
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
