@@ -152,6 +152,23 @@ class Config:
     def num_local(self) -> int:
         return self.num_experts if self.num_local_experts is None else self.num_local_experts
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_by_ref", None)
+
+    def ref(self):
+        """A reference to the C structure for a call, built again after a field
+        was set (building it takes 1 us of a small call's 6)."""
+        by_ref = self.__dict__.get("_by_ref")
+        if by_ref is None:
+            by_ref = ctypes.byref(self.c())
+            if isinstance(self.act_gs_static, tuple):   # anything else could change unseen
+                self.__dict__["_by_ref"] = by_ref
+        return by_ref
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_by_ref"}
+
     def c(self) -> CConfig:
         if self.fmt not in FMTS:
             raise ValueError(f"unknown format {self.fmt!r}")
@@ -414,14 +431,18 @@ def group_product(fmt: str, a, a_scales, w, w_scales, offsets, out, row_ids=None
                                  _stream()), "moe_group_product")
 
 
+@functools.lru_cache(maxsize=None)
+def _dtypes() -> dict:
+    import torch
+    return {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
 def _dtype(t, name: str) -> int:
     """MOE_DTYPE of a bf16 or fp32 tensor."""
-    import torch
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    if t.dtype == torch.float32:
-        return DTYPE_F32
-    raise ValueError(f"{name} must be bfloat16 or float32")
+    dt = _dtypes().get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    return dt
 
 
 def group_matvec(fmt: str, x, w, w_scales, offsets, out, gs=None, gs_group: int = 1, gs_stride: int = 1, row_ids=None,
@@ -444,8 +465,7 @@ def group_matvec(fmt: str, x, w, w_scales, offsets, out, gs=None, gs_group: int 
         if gs_group < 1 or N % gs_group:
             raise ValueError("N must be a multiple of gs_group")
         _check_gs(gs, G * gs_group, gs_group, gs_stride)
-    cc = None if swiglu is None else ctypes.byref(swiglu.c())
-    _ok(load().moe_group_matvec(cc, FMTS[fmt], _dtype(x, "x"), _ptr(x, None, None, "x"), rows,
+    _ok(load().moe_group_matvec(None if swiglu is None else swiglu.ref(), FMTS[fmt], _dtype(x, "x"), _ptr(x, None, None, "x"), rows,
                                 _ptr(row_ids, torch.int32, (M,), "row_ids"), id_div, M,
                                 _ptr(w, torch.uint8, (G, N, _code_cols(fmt, K)), "w"),
                                 _ptr(w_scales, torch.uint8, (G, N, _scale_cols(fmt, K)), "w_scales"),
@@ -464,9 +484,7 @@ def norm_forward(x, weight, y=None, residual=None, res_out=None, rstd=None, eps:
     fp32; weight [cols] and rstd [T] fp32.  Without cfg no codes are written."""
     import torch
     if isinstance(cfg, str):
-        cfg, cc = _default_config(cfg)
-    else:
-        cc = None if cfg is None else cfg.c()
+        cfg = _default_config(cfg)[0]
     T, cols = x.shape
     res = residual if residual is not None else res_out
     res_type = None if res is None else res.dtype
@@ -477,7 +495,7 @@ def norm_forward(x, weight, y=None, residual=None, res_out=None, rstd=None, eps:
                _ptr(row_gs, torch.float32, (T,), "row_gs") if cfg.fmt == "nvfp4" else None)
     elif codes is not None or scales is not None or row_gs is not None:
         raise ValueError("codes, scales and row_gs need cfg")
-    _ok(load().moe_norm_forward(None if cc is None else ctypes.byref(cc), _dtype(x, "x"), _ptr(x, None, None, "x"),
+    _ok(load().moe_norm_forward(None if cfg is None else cfg.ref(), _dtype(x, "x"), _ptr(x, None, None, "x"),
                                 _dtype(x if res is None else res, "residual"),
                                 _ptr(residual, res_type, (T, cols), "residual"), T, cols,
                                 _ptr(weight, torch.float32, (cols,), "weight"), eps,
@@ -650,8 +668,7 @@ def forward_quantized(cfg: Config, codes, scales, topk_ids, topk_w, weights, out
         if len(events) != 2 * len(STAGES):
             raise ValueError("events must hold 2 per stage")
         ev = (ctypes.c_void_p * len(events))(*[e.cuda_event if e is not None else None for e in events])
-    cc = cfg.c()
-    _ok(load().moe_forward_quantized(ctypes.byref(cc), _ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, H)), "codes"),
+    _ok(load().moe_forward_quantized(cfg.ref(), _ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, H)), "codes"),
                                      _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, H)), "scales"),
                                      _ptr(row_gs, torch.float32, (T,), "row_gs") if cfg.fmt == "nvfp4" else None, T,
                                      _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),

@@ -103,7 +103,10 @@ struct Wide<float, false> {
   typedef v4f V __attribute__((aligned(4)));
 };
 
-// NT: the hint for bytes that are used once (see kStreamBytes).
+// NT: the hint for bytes that are used once (see kStreamBytes).  fp32 does
+// without: a lane's 32 bytes are two accesses, and the hint gives the line away
+// between them (norm of an fp32 stream 412 us with it, 394 without; 16384 x 8
+// fp32 rows combined 420 and 388).
 template <bool FULL, bool NT>
 __device__ inline void load8(Raw8<uint16_t>& r, const uint16_t* p) {
   const auto* q = reinterpret_cast<const typename Wide<uint16_t, FULL>::V*>(p);
@@ -112,8 +115,8 @@ __device__ inline void load8(Raw8<uint16_t>& r, const uint16_t* p) {
 template <bool FULL, bool NT>
 __device__ inline void load8(Raw8<float>& r, const float* p) {
   const auto* q = reinterpret_cast<const typename Wide<float, FULL>::V*>(p);
-  r.a = NT ? __builtin_nontemporal_load(q) : *q;
-  r.b = NT ? __builtin_nontemporal_load(q + 1) : q[1];
+  r.a = *q;
+  r.b = q[1];
 }
 template <bool FULL, bool NT>
 __device__ inline void store8(uint16_t* p, const Raw8<uint16_t>& r) {
@@ -124,13 +127,8 @@ __device__ inline void store8(uint16_t* p, const Raw8<uint16_t>& r) {
 template <bool FULL, bool NT>
 __device__ inline void store8(float* p, const Raw8<float>& r) {
   auto* q = reinterpret_cast<typename Wide<float, FULL>::V*>(p);
-  if constexpr (NT) {
-    __builtin_nontemporal_store(r.a, q);
-    __builtin_nontemporal_store(r.b, q + 1);
-  } else {
-    q[0] = r.a;
-    q[1] = r.b;
-  }
+  q[0] = r.a;
+  q[1] = r.b;
 }
 __device__ inline void set(Raw8<uint16_t>& r, const float* v) {
   r.w = v4u{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};

@@ -39,6 +39,7 @@ CASES = [
     (1, 1, 1, 1, 1), (1, 1, 8, 0, 3), (1, 8, 64, 8, 8), (3, 2, 7, 4, 6), (5, 3, 40, 9, 20), (17, 4, 1003, 50, 68),
     (6, 32, 96, 150, 192), (33, 8, 2304, 200, 264), (20, 8, 4608, 160, 160), (4, 5, 8200, 13, 20), (2, 3, 65536, 5, 6),
     (2, 2, 65535, 3, 4), (300, 6, 136, 900, 1800), (9, 3, 520, 0, 0),
+    (1024, 2, 72, 1500, 2048), (1030, 3, 1003, 2000, 3090), (1025, 2, 8, 2050, 2050), (1024, 1, 5, 700, 1024),
 ]
 
 
