@@ -182,11 +182,17 @@ def _ok(status: int, what: str) -> None:
         raise MoeError(status, what)
 
 
-def _stream() -> int:
-    """The current stream's handle.  The raw accessor: building a Stream object
-    takes 3 us, more than everything else around a small call."""
+@functools.lru_cache(maxsize=None)
+def _accessors():
     import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _stream() -> int:
+    """The current stream's handle.  The raw accessors: building a Stream object
+    takes 3 us, more than everything else around a small call."""
+    stream, device = _accessors()
+    return stream(device())
 
 
 def _ptr(t, dtype=None, shape=None, name="tensor"):
@@ -533,10 +539,17 @@ def norm_backward(dy, res, weight, rstd, d_res, ws=None, d_res_out=None, dx=None
 
 def _slots(pair_pos, T: int) -> int:
     """Slots of a token in pair_pos ([T, top_k] or flat)."""
-    n = pair_pos.numel()
-    if pair_pos.dim() == 2 and pair_pos.shape[0] != T or T > 0 and (n == 0 or n % T):
+    shape = pair_pos.shape
+    if len(shape) == 2 and shape[0] == T:
+        k = shape[1]
+    else:
+        n = pair_pos.numel()
+        if len(shape) != 1 or T > 0 and n % T:
+            raise ValueError(f"pair_pos must hold top_k positions for each of {T} tokens")
+        k = n // T if T > 0 else 1
+    if k < 1:
         raise ValueError(f"pair_pos must hold top_k positions for each of {T} tokens")
-    return n // T if T > 0 else 1
+    return k
 
 
 def sort_rows(x, pair_pos, out) -> None:

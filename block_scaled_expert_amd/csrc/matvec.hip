@@ -20,120 +20,21 @@
 //    16x16x32 took 2, and 612 us where this takes 556);
 //  - scales are loaded four chunks at a time (Scales).
 // x, in bf16, waits in LDS; an fp32 x as three bf16 parts whose sum it is.
-// Products are exact and sums fp32; gs is applied to the sums.  A row's sums do
-// not depend on the other rows of its group or call; on how many waves share
-// the chunks they do (KS, from the sizes of the call).
+// Products are exact and sums fp32; gs is applied to the sums.  A row's bits do
+// not depend on which other rows its group or call has, but follow the sizes of
+// the call: which kernel takes it, and how many waves share the chunks (KS).
 //
 // Measured (us; TB/s of the weights in use): 64 tokens' gate/up with SwiGLU, 512
 // rows over 283 of 384 groups of 4608 x 4608, NVFP4 556 to 613 on different
-// machines (5.5 to 6.1), MXFP4 549; 192 tokens' down, 1536 rows over 377
-// groups of 4608 x 2304, MXFP4 417 (5.1), with fp32 rows 553 (three times the
-// products and x reads); one token's gate/up, 8 groups, 23.5 (4.1).
-#include "group_product.h"
+// machines (5.5 to 6.1), MXFP4 549; one token's gate/up, 8 groups, 23.5 (4.1).
+// With more rows, or fp32 rows (three times the products and x reads), the
+// kernel of matvec_wide.hip is ahead.
+#include "matvec.h"
 
 namespace moe {
 
 namespace {
 
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-
-// Codes of two blocks of 32 per lane, as loaded (RawW's order), and, unless
-// scales come in fours of chunks (Scales), row r's scales of them.
-template <int FMT>
-struct Chunk {
-  v4u q[2];
-  uint32_t sc;     // MXFP4: 2 bytes, NVFP4: 4
-};
-
-// WHOLE: rows of whole chunks.  Otherwise the row may end inside a chunk, and
-// scales are loaded block by block.
-template <int FMT, bool WHOLE>
-__device__ inline void load_chunk(Chunk<FMT>& W, Buf wq, Buf ws, const WLane& l, bool on, uint32_t base, uint32_t srow, int c) {
-  const int blk = kChunkBlocks * c;
-  const uint32_t off = on && (WHOLE || blk + l.at < l.nb) ? l.off + base + 16 * blk : kNowhere;
-  W.q[0] = buf16<true>(wq, off);
-  W.q[1] = buf16<true>(wq, off + l.row8);
-  if constexpr (!WHOLE) {
-    constexpr int S = FMT == 1 ? 2 : 1;      // scale bytes of a block
-    const uint32_t so = S * (srow + blk + kU * l.b);
-    const uint32_t at0 = on && blk + kU * l.b < l.nb ? so : kNowhere, at1 = on && blk + kU * l.b + 1 < l.nb ? so + S : kNowhere;
-    if constexpr (FMT == 1) {
-      const uint32_t a = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ws, (int)at0, 0, 0);
-      const uint32_t b = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ws, (int)at1, 0, 0);
-      W.sc = a | b << 16;
-    } else {
-      const uint32_t a = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)at0, 0, 0);
-      const uint32_t b = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(ws, (int)at1, 0, 0);
-      W.sc = a | b << 8;
-    }
-  }
-}
-
-// Scales of four chunks of 16 rows at a time.  One by one they are 16 (NVFP4)
-// or 8 bytes of a line per row and chunk, and fetching 16 lines for them costs
-// as much as the codes' 16: 512 rows over 283 groups of 4608 x 4608 NVFP4 took
-// 732 us that way, 549 with no scales loaded at all.  Here lane (r, b) loads row
-// r's scales of chunk b (16 or 8 bytes), and swaps between the four rows of
-// lanes hand lane (r, b) what it needs of each chunk.
-template <int FMT>
-struct Scales {
-  v4u next;            // as loaded; MXFP4 uses two words
-  uint32_t now[4];     // of the chunks to come, the nearest first
-
-  // this lane's chunk: number `at` of the view's, row after row
-  __device__ inline void load(Buf ws, bool on, uint32_t at) {
-    constexpr int kBytes = FMT == 1 ? 16 : 8;
-    const uint32_t off = on ? kBytes * at : kNowhere;
-    if constexpr (FMT == 1) {
-      next = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(ws, (int)off, 0, 0));
-    } else {
-      typedef unsigned v2u __attribute__((ext_vector_type(2)));
-      const v2u w = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(ws, (int)off, 0, 0));
-      next[0] = w[0];
-      next[1] = w[1];
-    }
-  }
-  __device__ inline void take(int b) {
-    if constexpr (FMT == 1) {
-      // 4 x 4 words across the rows of lanes: halves, then neighbours
-      const auto a = __builtin_amdgcn_permlane32_swap(next[0], next[2], false, false);
-      const auto c = __builtin_amdgcn_permlane32_swap(next[1], next[3], false, false);
-      const auto e = __builtin_amdgcn_permlane16_swap(a[0], c[0], false, false);
-      const auto f = __builtin_amdgcn_permlane16_swap(a[1], c[1], false, false);
-      now[0] = e[0];
-      now[1] = e[1];
-      now[2] = f[0];
-      now[3] = f[1];
-    } else {
-      // lanes b = 0, 1 share a chunk's first word, 2, 3 its second
-      const auto a = __builtin_amdgcn_permlane32_swap(next[0], next[1], false, false);
-      const auto e = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
-      const auto f = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
-      const int half = 16 * (b & 1);
-      now[0] = e[0] >> half;
-      now[1] = e[1] >> half;
-      now[2] = f[0] >> half;
-      now[3] = f[1] >> half;
-    }
-  }
-  __device__ inline uint32_t pop() {
-    const uint32_t s = now[0];
-    now[0] = now[1];
-    now[1] = now[2];
-    now[2] = now[3];
-    return s;
-  }
-};
-
-// Eight codes (low nibble first) as bf16, times the power of two in scale's
-// exponent (an E8M0 byte moved there: 255 gives NaN).
-typedef short v4s __attribute__((ext_vector_type(4)));
-typedef short v8s __attribute__((ext_vector_type(8)));
-__device__ inline v8s widen(uint32_t w, float scale) {
-  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
-  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
-  return __builtin_bit_cast(v8s, v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]});
-}
 __device__ inline v4s lo4(v8s v) { return v4s{v[0], v[1], v[2], v[3]}; }
 __device__ inline v4s hi4(v8s v) { return v4s{v[4], v[5], v[6], v[7]}; }
 
@@ -158,22 +59,6 @@ __device__ inline float lanes_by_8(const v4f (&s)[2], int r) {
   return bits_f(w[0]) + bits_f(w[1]);
 }
 
-// x as hi + mid + lo, each a bf16 (the upper 16 bits of what is left); inf and
-// NaN in hi alone.
-__device__ inline void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  if (!(fabsf(x) < INFINITY)) {
-    hi = __builtin_bit_cast(uint16_t, (__bf16)x);
-    mid = lo = 0;
-    return;
-  }
-  const uint32_t h = f_bits(x) & 0xFFFF0000u;
-  const float r = x - bits_f(h);
-  const uint32_t m = f_bits(r) & 0xFFFF0000u;
-  hi = h >> 16;
-  mid = m >> 16;
-  lo = f_bits(r - bits_f(m)) >> 16;
-}
-
 }  // namespace
 
 // F32: x in fp32.  GLU: the upper half of the waves takes the up rows of the
@@ -191,7 +76,7 @@ __global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, in
   const int width = GLU ? p.N / 2 : p.N;            // columns of out
   const int cols = GLU ? 8 * WC : 16 * WC;          // of a tile
 
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, threads = blockDim.x;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   if (wave == 0) {                                  // one wave looks for the item
     Item it;
     if (!find_item<kRows>(p, (width + cols * NT - 1) / (cols * NT), blockIdx.x, it)) it.rows = 0;
@@ -242,56 +127,12 @@ __global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, in
 #pragma unroll
   for (int j = 0; j < PF; j++) load_next(ring[j]);
 
-  // x in panels of as many chunks as the item's rows leave room for; rows are
-  // 16 bytes apart beyond a multiple of 512, which spreads them over the banks
-  const int most = max((lds_bytes / (PLANES * rows) - 16) / (2 * kChunkK), 1);
-  const int panels = (chunks + most - 1) / most, panel = (chunks + panels - 1) / panels;
-  const int stride = 2 * kChunkK * panel + 16, plane = stride * rows;
-  auto stage_x = [&](int p0, int pn) {
-    // a wave per row and run of 512 k (64 pieces of 8), if there are enough
-    const int runs = (pn + 1) / 2, waves = threads >> 6;
-    int row = wave, run = 0;
-    for (;;) {
-      while (row >= rows) {
-        row -= rows;
-        run++;
-      }
-      if (run >= runs) break;
-      const int q = 64 * run + lane, k = kChunkK * p0 + 8 * q, s = max(src[row], 0);
-      const bool in = q < pn * (kChunkK / 8);
-      v4u hi = v4u{0, 0, 0, 0}, mid = hi, lo = hi;
-      if (in && (WHOLE || k < p.K)) {               // zeros past the end of k
-        if constexpr (F32) {
-          const v4f* x = reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(p.a) + (size_t)s * p.K + k);
-          const v4f u = x[0], v = x[1];
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            uint32_t h0, m0_, l0, h1, m1, l1;
-            split3(j < 2 ? u[2 * j] : v[2 * j - 4], h0, m0_, l0);
-            split3(j < 2 ? u[2 * j + 1] : v[2 * j - 3], h1, m1, l1);
-            hi[j] = h0 | h1 << 16;
-            mid[j] = m0_ | m1 << 16;
-            lo[j] = l0 | l1 << 16;
-          }
-        } else {
-          hi = *reinterpret_cast<const v4u*>(reinterpret_cast<const uint16_t*>(p.a) + (size_t)s * p.K + k);
-        }
-      }
-      uint8_t* const to = lds + row * stride + 16 * q;
-      if (in) {
-        *reinterpret_cast<v4u*>(to) = hi;
-        if constexpr (F32) {
-          *reinterpret_cast<v4u*>(to + plane) = mid;
-          *reinterpret_cast<v4u*>(to + 2 * plane) = lo;
-        }
-      }
-      row += waves;
-    }
-  };
+  const Panels pan(lds_bytes, PLANES, rows, chunks);
+  const int panel = pan.size, stride = pan.stride, plane = pan.plane;
+  const bool one = pan.n == 1;
   lds_barrier();                                    // src is written
-  const bool one = panels == 1;
   if (one) {
-    stage_x(0, chunks);
+    stage_x<F32, WHOLE>(p, src, rows, 0, chunks, lds, stride, plane);
     lds_barrier();
   }
   // lane (r, b) of quad k has x row 4 k + r % 4 and the block of 32 that it has codes of;
@@ -345,7 +186,7 @@ __global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, in
       if (t < tiles) {
         if (!one && xc == 0) {                      // KS is 1: every wave is at the same chunk
           lds_barrier();                            // the last panel has been read
-          stage_x(i, min(panel, chunks - i));
+          stage_x<F32, WHOLE>(p, src, rows, i, min(panel, chunks - i), lds, stride, plane);
           lds_barrier();
         }
         if constexpr (WHOLE) {
@@ -482,8 +323,23 @@ static void launch_fmt(const MatvecArgs& a, hipStream_t stream) {
   }
 }
 
+// By the mean group, and by tiles of 64 columns of 16 rows (fewer leave CUs idle
+// there).  us, quads / wide, 4608 x 4608 NVFP4 bf16: 64 rows of one group 24.8/29.6
+// (360 tiles), 96 of 8 groups 47.0/44.1 (1008), 16384 columns 16 rows 21.9/30.0
+// (512), 32 rows 30.2/30.1 (768), 64 rows 55.9/40.7.  384 groups of 4608 x 2304,
+// mean 1.3, 4, 6, 8, 12 rows: MXFP4 bf16 295/-, 415/407, -, 550/459, 714/520;
+// fp32 333/293, 548/431, 705/495, -, 1219/619; NVFP4 fp32 370/386 (1.3), 591/553
+// (4), bf16 605/521 (8), 788/590 (12), gate/up with SwiGLU 580/596 (1.3), 823/801 (4).
+static bool wide_rows(const MatvecArgs& a) {
+  const long tiles = (long)max_tiles(a.p, 16) * ceil_div(a.swiglu ? a.p.N / 2 : a.p.N, a.swiglu ? 32 : 64);
+  const long M = a.p.M, G = a.p.G;
+  if (tiles < 768) return false;
+  return a.dtype == 1 ? (a.fmt == 4 ? 2 * M > G : M > 2 * G) : M > 3 * G;
+}
+
 int launch_group_matvec(const MatvecArgs& a, hipStream_t stream) {
   if (a.p.M <= 0) return 0;
+  if (wide_rows(a)) return launch_matvec_wide(a, stream);
   if (a.fmt == 1) launch_fmt<1>(a, stream);
   else launch_fmt<4>(a, stream);
   return hipGetLastError() == hipSuccess ? 0 : -1;

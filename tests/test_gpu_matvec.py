@@ -122,6 +122,22 @@ def test_product(gpu_lib, G, M, N, K, kind, fmt, dtype, out_dtype):
     _check(gpu_lib, np.random.default_rng(G * 7919 + M * 31 + N + K), fmt, dtype, out_dtype, G, M, N, K, kind)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("G,M,N,K,kind,glu", [
+    # two and four sets of waves on the chunks; whole rows of chunks or not
+    (8, 20, 1200, 1024, "uneven", False), (2, 9, 600, 1536, "uneven", True), (3, 9, 700, 800, "uneven", False),
+    # many tiles a workgroup, 1 row a group
+    (384, 400, 1500, 256, "uneven", False), (384, 450, 1800, 256, "uneven", True), (384, 420, 1500, 96, "uneven", False),
+    # more rows: 16 at a time, in several panels, one and two tiles in turn
+    (48, 300, 1100, 512, "uneven", False), (20, 100, 3000, 2304, "uneven", False), (24, 130, 2100, 1280, "uneven", True),
+    (384, 1600, 1500, 256, "uneven", False), (30, 200, 1600, 1056, "one", False), (300, 1300, 1210, 160, "uneven", True),
+])
+def test_larger_calls(gpu_lib, G, M, N, K, kind, glu, fmt, dtype):
+    _check(gpu_lib, np.random.default_rng(G * 7919 + M * 31 + N + K), fmt, dtype, "f32", G, M, N, K, kind,
+           glu=gpu_lib.Config(cap=7.0) if glu else None)
+
+
 @pytest.mark.parametrize("cap_form", [0, 1, 2, 3])
 @pytest.mark.parametrize("dtype,out_dtype", [("bf16", "f32"), ("f32", "bf16")])
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
