@@ -76,6 +76,7 @@ struct NormArgs {
   const void* x;            // [T][cols]
   const void* res;          // [T][cols] nullable
   int dtype, res_dtype, T, cols;
+  double inv_cols;          // 1 / cols, set by the launcher
   const float* weight;      // [cols]
   float eps;
   void* res_out;            // [T][cols] nullable
@@ -101,7 +102,7 @@ struct NormGradArgs {
   int pitch;
 };
 size_t norm_ws_bytes(int T, int cols);
-int launch_norm_forward(const NormArgs& a, hipStream_t stream);
+int launch_norm_forward(NormArgs a, hipStream_t stream);
 int launch_norm_backward(NormGradArgs a, float* d_weight, void* ws, hipStream_t stream);
 
 // Tokens sorted by expert and back (rows.hip).

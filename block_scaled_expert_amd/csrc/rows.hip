@@ -10,6 +10,10 @@
 // once, addressed by token (reading by expert row instead would fetch a token
 // k times).  A wavefront has one token, so positions and weights are uniform;
 // pairs elsewhere are skipped before any load.  Sums are fp32 in slot order.
+// Measured, 16384 tokens of 4608, 8 slots (TB/s of what has to move): all local in
+// bf16, sort, combine and both gradients 1300 us in all (5.1), combine's gradient
+// 500 (5.1); an eighth local with fp32 expert rows 332 to 380 in all (4.8 to 5.5).
+// 64 tokens 2.8 (sort) and 4.2 (combine of fp32 rows).
 #include "operators.h"
 #include "row_io.h"
 
@@ -160,9 +164,10 @@ __global__ __launch_bounds__(1024) void k_combine_rows_backward(RowsArgs a) {
 
 namespace {
 
-// Workgroups of a call that has a row's columns to itself: a whole row each for
-// many tokens, so that positions are fetched once a row; for few tokens a run of
-// 8 columns a thread, so that there are more of them.
+// Workgroups of the sort and of the combine: a whole row each for many tokens, so
+// that a row's positions are fetched once and there is more in flight behind them
+// (an eighth local 392 us in all, in runs 432; 8 fp32 rows a token 842, in runs
+// 1124); for few tokens a run of 8 columns a thread, so that there are more.
 constexpr int kManyTokens = 1024;
 struct Shape {
   int waves, pieces, runs;

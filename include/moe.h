@@ -393,8 +393,8 @@ int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, con
 /* The layer's input in one pass: residual addition, root-mean-square norm
  * and, with cfg not NULL, the quantization of the normed rows.
  *   s = x + residual            (in fp32, rounded to res_dtype; x without residual)
- *   r = 1 / sqrt(mean over the row of s^2 + eps)
- *   y = s r weight              (in fp32, rounded to dtype)
+ *   r = 1 / sqrt(mean over the row of s^2 + eps)   (squares summed in 64 bits)
+ *   y = s r weight              (the exact value rounded to fp32, then to dtype)
  *  x, y [T][cols] of dtype; residual and res_out [T][cols] of res_dtype, which
  *  is dtype or fp32 (fp32 x with a bf16 stream: MOE_ERR_INVALID_ARG); weight
  *  [cols] fp32; eps > 0, finite.  residual, res_out (s) and rstd (r, [T]

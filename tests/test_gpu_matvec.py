@@ -110,7 +110,7 @@ CASES = [
     (1, 17, 130, 256, "even"), (3, 7, 64, 160, "uneven"), (5, 51, 1003, 352, "uneven"), (16, 40, 96, 2304, "uneven"),
     (48, 130, 256, 1184, "uneven"), (7, 70, 130, 640, "one"), (2, 200, 520, 768, "even"), (1, 33, 66, 4608, "even"),
     (1024, 60, 33, 64, "uneven"), (1, 2, 40, 20480, "even"), (1, 13, 40, 9248, "even"), (300, 2000, 70, 96, "uneven"),
-    (64, 600, 1300, 64, "even"),
+    (64, 600, 1300, 64, "even"), (1, 2, 3, 262144, "even"), (1, 3, 70000, 64, "even"),
 ]
 
 

@@ -177,6 +177,34 @@ def test_extreme_rows(gpu_lib):
         assert (np.abs(_f64(y[i]) - want) <= (ADDS / 2 + 7) * U * np.abs(want)).all(), i
 
 
+@pytest.mark.parametrize("size", [1e30, 1e-15, 1e-25])
+def test_squares_beyond_fp32(gpu_lib, size):
+    """Rows whose squares leave fp32's range on either side (eps as far down)."""
+    import torch
+    cols, eps = 1003, 1e-38 if size < 1 else 1e-6
+    x = _rand((3, cols), 2, "f32") * size
+    w = 1.0 + 0.1 * _rand((cols,), 3, "f32")
+    y, rstd = torch.empty_like(x), torch.empty(3, device="cuda")
+    gpu_lib.norm_forward(x, w, y, rstd=rstd, eps=eps)
+    want, wr = S.norm_forward(_f64(x), _f64(w), float(np.float32(eps)))
+    assert (np.abs(_f64(y) - want) <= 4 * U * np.abs(want) + TINY).all()
+    assert (np.abs(_f64(rstd) - wr) <= 2 * U * wr).all()
+
+
+def test_a_normed_row_is_the_exact_one_rounded(gpu_lib):
+    """y is the 64-bit result rounded to fp32 and then to the type, so the codes
+    are those of the exact row."""
+    import torch
+    T, cols = 200, 4608
+    x, r = _rand((T, cols), 1, "bf16", loud=True), _rand((T, cols), 2, "bf16", 3.0)
+    w = 1.0 + 0.1 * _rand((cols,), 3, "f32")
+    y, s = torch.empty_like(x), torch.empty_like(x)
+    gpu_lib.norm_forward(x, w, y, residual=r, res_out=s)
+    want = torch.from_numpy(S.norm_forward(_f64(s), _f64(w), float(np.float32(1e-6)))[0]).float().bfloat16()
+    # off only where fp32 itself rounds to the other side: the carried errors leave 2^-46, below 1 in 10^6 elements
+    assert int((y.cpu() != want).sum()) <= 1
+
+
 def test_offsets_into_larger_arrays(gpu_lib):
     """Rows at addresses that are no multiple of 16 bytes; what lies around the
     outputs stays."""
