@@ -188,11 +188,15 @@ def _accessors():
     return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _stream() -> int:
-    """The current stream's handle.  The raw accessors: building a Stream object
-    takes 3 us, more than everything else around a small call."""
+def _stream(t=None) -> int:
+    """The current stream's handle; t, one of a call's tensors, must be on the
+    current device.  The raw accessors: building a Stream object takes 3 us, more
+    than everything else around a small call."""
     stream, device = _accessors()
-    return stream(device())
+    current = device()
+    if t is not None and t.get_device() != current:
+        raise ValueError(f"tensors must be on the current device ({current}), got one on {t.get_device()}")
+    return stream(current)
 
 
 def _ptr(t, dtype=None, shape=None, name="tensor"):
@@ -477,7 +481,7 @@ def group_matvec(fmt: str, x, w, w_scales, offsets, out, gs=None, gs_group: int 
                                 _ptr(w_scales, torch.uint8, (G, N, _scale_cols(fmt, K)), "w_scales"),
                                 _ptr(gs, torch.float32, None, "gs") if nv else None, gs_group, gs_stride, G, N, K,
                                 _ptr(offsets, torch.int32, (G + 1,), "offsets"), _dtype(out, "out"),
-                                _ptr(out, None, (M, N if swiglu is None else N // 2), "out"), _stream()),
+                                _ptr(out, None, (M, N if swiglu is None else N // 2), "out"), _stream(x)),
         "moe_group_matvec")
 
 
@@ -506,7 +510,7 @@ def norm_forward(x, weight, y=None, residual=None, res_out=None, rstd=None, eps:
                                 _ptr(residual, res_type, (T, cols), "residual"), T, cols,
                                 _ptr(weight, torch.float32, (cols,), "weight"), eps,
                                 _ptr(res_out, res_type, (T, cols), "res_out"), _ptr(y, x.dtype, (T, cols), "y"),
-                                _ptr(rstd, torch.float32, (T,), "rstd"), *enc, _stream()), "moe_norm_forward")
+                                _ptr(rstd, torch.float32, (T,), "rstd"), *enc, _stream(x)), "moe_norm_forward")
 
 
 def norm_workspace_size(T: int, cols: int) -> int:
@@ -533,7 +537,7 @@ def norm_backward(dy, res, weight, rstd, d_res, ws=None, d_res_out=None, dx=None
                                  _ptr(rstd, torch.float32, (T,), "rstd"), _ptr(d_res, res.dtype, (T, cols), "d_res"),
                                  _ptr(dx, dy.dtype, (T, cols), "dx"),
                                  _ptr(d_weight, torch.float32, (cols,), "d_weight"),
-                                 _ptr(ws, torch.uint8, None, "ws"), 0 if ws is None else ws.numel(), _stream()),
+                                 _ptr(ws, torch.uint8, None, "ws"), 0 if ws is None else ws.numel(), _stream(dy)),
         "moe_norm_backward")
 
 
@@ -560,7 +564,7 @@ def sort_rows(x, pair_pos, out) -> None:
     M = out.shape[0]
     _ok(load().moe_sort_rows(_dtype(x, "x"), _ptr(x, None, None, "x"), T, _slots(pair_pos, T), cols,
                              _ptr(pair_pos, torch.int32, None, "pair_pos"), M, _ptr(out, x.dtype, (M, cols), "out"),
-                             _stream()), "moe_sort_rows")
+                             _stream(x)), "moe_sort_rows")
 
 
 def sort_rows_backward(d_out, pair_pos, dx) -> None:
@@ -570,7 +574,7 @@ def sort_rows_backward(d_out, pair_pos, dx) -> None:
     M = d_out.shape[0]
     _ok(load().moe_sort_rows_backward(_dtype(dx, "dx"), _ptr(d_out, dx.dtype, (M, cols), "d_out"), M,
                                       _ptr(pair_pos, torch.int32, None, "pair_pos"), T, _slots(pair_pos, T), cols,
-                                      _ptr(dx, None, None, "dx"), _stream()), "moe_sort_rows_backward")
+                                      _ptr(dx, None, None, "dx"), _stream(dx)), "moe_sort_rows_backward")
 
 
 def combine_rows(y, pair_pos, topk_w, out) -> None:
@@ -583,7 +587,7 @@ def combine_rows(y, pair_pos, topk_w, out) -> None:
     _ok(load().moe_combine_rows(_dtype(y, "y"), _ptr(y, None, (M, cols), "y"), M,
                                 _ptr(pair_pos, torch.int32, None, "pair_pos"),
                                 _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols, _dtype(out, "out"),
-                                _ptr(out, None, None, "out"), _stream()), "moe_combine_rows")
+                                _ptr(out, None, None, "out"), _stream(out)), "moe_combine_rows")
 
 
 def combine_rows_backward(d_out, y, pair_pos, topk_w, dy, d_topk_w=None) -> None:
@@ -600,7 +604,7 @@ def combine_rows_backward(d_out, y, pair_pos, topk_w, dy, d_topk_w=None) -> None
                                          _ptr(y, None, (M, cols), "y"), M, _ptr(pair_pos, torch.int32, None, "pair_pos"),
                                          _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols,
                                          _ptr(dy, rows.dtype, (M, cols), "dy"),
-                                         _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream()),
+                                         _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream(d_out)),
         "moe_combine_rows_backward")
 
 
@@ -687,7 +691,7 @@ def forward_quantized(cfg: Config, codes, scales, topk_ids, topk_w, weights, out
                                      _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
                                      _ptr(topk_w, torch.float32, (T, k), "topk_w"), ctypes.byref(cw),
                                      _ptr(out, torch.bfloat16, (T, H), "out"), _ptr(ws, torch.uint8, None, "ws"),
-                                     ws.numel(), _stream(), ev), "moe_forward_quantized")
+                                     ws.numel(), _stream(codes), ev), "moe_forward_quantized")
 
 
 def forward_noalloc(cfg: Config, x, topk_ids, topk_w, weights, out) -> None:

@@ -377,6 +377,9 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
  *  gs + 2, gs_group 1, gs_stride 3.  MXFP4 reads none of the three.  NaN
  *  scale bytes (E8M0 255, E4M3 0x7F and 0xFF; never written by the encoder)
  *  give NaN.
+ *  An MXFP4 weight of 2^128 and more (no finite weight is encoded as one) is
+ *  infinite.  fp32 x enters as three bf16 parts, whole down to 2^-110; below,
+ *  what lies under 2^-133 is dropped.
  *  offsets [G+1] ascending, within [0, M] (values outside are clamped); a
  *  group may be empty.  out: rows in no group are not written.  A row whose
  *  source lies outside [0, x_rows) is zero.  out may not overlap the inputs.
@@ -384,7 +387,8 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
  *  <= 1024, M and x_rows at most 2^26, (G + M / 8) ceil(N / 64) at most
  *  2^22.  x, w and out 16-byte aligned, the other arrays 4.
  * No workspace; one launch.  Any number of rows is right; what it is made for
- * is groups of up to 8, each further 8 read the group's weights again. */
+ * is groups of up to 8 or 16 (by the mean group), each further 8 or 16 read the
+ * group's weights again. */
 int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, const void* x, int32_t x_rows,
                      const int32_t* row_ids, int32_t id_div, int32_t M, const uint8_t* w, const uint8_t* w_scales,
                      const float* gs, int32_t gs_group, int32_t gs_stride, int32_t G, int32_t N, int32_t K,

@@ -333,3 +333,26 @@ def test_training_step_in_a_graph(gpu_lib):
         torch.cuda.synchronize()
         for name in ("out", "dw", "dn", "d_res", "d_gain"):
             assert torch.equal(getattr(p, name), getattr(eager, name)), (rep, name)
+
+
+def test_tensors_of_another_device_are_refused(gpu_lib, monkeypatch):
+    """Every call launches on the current device: tensors of another one are an
+    error before anything is enqueued."""
+    import torch
+    bse = gpu_lib
+    x, o, w = torch.zeros((2, 32), device="cuda"), torch.ones((2, 32), device="cuda"), torch.ones(32, device="cuda")
+    pos, tw, r = torch.zeros((2, 1), dtype=torch.int32, device="cuda"), torch.ones((2, 1), device="cuda"), torch.ones(2, device="cuda")
+    codes, sc = (torch.zeros((1, 4, n), dtype=torch.uint8, device="cuda") for n in (16, 1))
+    off = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    cfg = bse.Config(fmt="mxfp4", hidden=32, num_experts=1, top_k=1)
+    bf = torch.zeros((2, 32), dtype=torch.bfloat16, device="cuda")
+    stream, device = bse._accessors()
+    monkeypatch.setattr(bse, "_accessors", lambda: (stream, lambda: device() + 1))
+    for call in (lambda: bse.norm_forward(x, w, o), lambda: bse.norm_backward(x, x, w, r, o),
+                 lambda: bse.sort_rows(x, pos, o), lambda: bse.sort_rows_backward(x, pos, o),
+                 lambda: bse.combine_rows(x, pos, tw, o), lambda: bse.combine_rows_backward(x, x, pos, tw, o),
+                 lambda: bse.group_matvec("mxfp4", x, codes, sc, off, o[:, :4].contiguous()),
+                 lambda: bse.forward_quantized(cfg, codes[0, :2], sc[0, :2], pos, tw, bse.CWeights(), bf, codes.view(-1))):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert (o == 1).all()
