@@ -17,7 +17,7 @@
 //    is done.  So lanes may hold codes of any row and block, as they were loaded,
 //    and an NVFP4 block's scale is applied to its 4 sums instead of its 16 codes
 //    (0.75 vector instructions a weight; widening and scaling each code for
-//    16x16x32 took 2, and 612 us where this takes 556);
+//    16x16x32 took 2, and 612 us where this took 556);
 //  - scales are loaded four chunks at a time (Scales).
 // x, in bf16, waits in LDS; an fp32 x as three bf16 parts whose sum it is.
 // Products are exact and sums fp32; gs is applied to the sums.  A row's bits do
@@ -25,8 +25,8 @@
 // the call: which kernel takes it, and how many waves share the chunks (KS).
 //
 // Measured (us; TB/s of the weights in use): 64 tokens' gate/up with SwiGLU, 512
-// rows over 283 of 384 groups of 4608 x 4608, NVFP4 556 to 613 on different
-// machines (5.5 to 6.1), MXFP4 549; one token's gate/up, 8 groups, 23.5 (4.1).
+// rows over 283 of 384 groups of 4608 x 4608, NVFP4 518 to 551 on different
+// machines (6.1 to 6.5), MXFP4 540; one token's gate/up, 8 groups, 23.5 (4.1).
 // With more rows, or fp32 rows (three times the products and x reads), the
 // kernel of matvec_wide.hip is ahead.
 #include "matvec.h"
@@ -278,34 +278,59 @@ __global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, in
 // 8 take 416.
 constexpr int kQuads = 2;
 
-// Waves of a workgroup and LDS, by tiles (64 columns of 8 rows at most):
-//  - up to 10240, 4 waves and 36 KiB, four workgroups a CU: with 8 waves and 76
-//    KiB the same work is handed out in larger pieces, which took 84 us instead
-//    of 68 for 4 tokens' gate/up, 229 instead of 219 for 16;
-//  - above, 8 waves and 76 KiB, in which 8 rows of k 4608 fit: where groups have
+// Waves of a workgroup and LDS, by tiles (64 columns of 8 rows at most).  A CU has
+// 160 KiB of LDS; SwiGLU's exchange takes 4 beside x.
+//  - up to 10240, 4 waves and 36 KiB, three or four workgroups a CU: with 8 waves
+//    and 74 KiB the same work is handed out in larger pieces, which took 84 us
+//    instead of 68 for 4 tokens' gate/up, 229 instead of 219 for 16;
+//  - above, 8 waves and 74 KiB, in which 8 rows of k 4608 fit: where groups have
 //    more than 3 rows, 4 waves bring x in again for every tile (1536 rows down
-//    in fp32 624 us instead of 553, gate/up 882 instead of 842);
+//    in fp32 624 us instead of 553, gate/up 882 instead of 842).  At 76 KiB only
+//    one workgroup with SwiGLU fits a CU: 64 tokens' gate/up 582 us instead of 551,
+//    with fp32 rows 767 instead of 686;
 //  - up to 256, where all of x fits, two sets of 2 waves share the chunks, up to
 //    128 four sets: there are not enough columns to go round (4608 x 4608, one
-//    row: 8.7 us instead of 11.8; 16384 columns 12.9 instead of 13.7).
-template <int FMT, bool F32, bool GLU, bool WHOLE>
-static void launch_one(const MatvecArgs& a, hipStream_t stream) {
-  const int width = GLU ? a.p.N / 2 : a.p.N, items = max_tiles(a.p, 4 * kQuads), chunks = ceil_div(a.p.K, kChunkK);
+//    row: 8.7 us instead of 11.8; 16384 columns 12.9 instead of 13.7; 4 rows in
+//    fp32 11.4 instead of 20.3).  8 fp32 rows fit as two items of 4, in sets of 4
+//    waves where one workgroup fills a CU's LDS (13.3 instead of 28.0 as one item,
+//    25.4 in sets of 2);
+//  - up to 512 (256) otherwise, what x needs up to 74 (150) KiB, as two workgroups
+//    a CU (one) leave it: 8 fp32 rows, 16384 x 4608, 28.3 us instead of 32.0.
+constexpr long kMostLds = 150 * 1024;
+template <int FMT, bool F32, bool GLU, bool WHOLE, int NQ>
+static void launch_rows(const MatvecArgs& a, hipStream_t stream) {
+  const int width = GLU ? a.p.N / 2 : a.p.N, items = max_tiles(a.p, 4 * NQ), chunks = ceil_div(a.p.K, kChunkK);
   const long tiles = (long)ceil_div(width, GLU ? 32 : 64) * items;
-  int WC = tiles <= 10240 ? 4 : 8, KS = 1, lds = (WC == 8 ? 76 : 36) * 1024;
+  int WC = tiles <= 10240 ? 4 : 8, KS = 1, lds = (WC == 8 ? 74 : 36) * 1024;
   // tiles a workgroup takes in turn, so that there remain about 1024 workgroups (2 to 4 a CU)
   const long nt = tiles * 4 / WC / 1024;
   const int NT = (int)(nt < 1 ? 1 : nt > 4 ? 4 : nt);
-  const int most = a.p.M < 4 * kQuads ? a.p.M : 4 * kQuads;   // rows of an item at most
+  const int most = a.p.M < 4 * NQ ? a.p.M : 4 * NQ;   // rows of an item at most
   const long need = (long)(F32 ? 3 : 1) * most * (2 * kChunkK * chunks + 16);
-  if (tiles <= 256 && need <= 80 * 1024 && chunks > 1) {
-    WC = 2;
+  if (tiles <= 256 && need <= kMostLds && chunks > 1) {
     KS = tiles <= 128 && chunks > 3 ? 4 : 2;
-    const int red = (KS - 1) * WC * kQuads * 2048;
+    WC = KS == 2 && need > 74 * 1024 ? 4 : 2;         // one workgroup a CU: as many as tiles
+    const int red = (KS - 1) * WC * NQ * 2048;
     lds = need > red ? (int)need : red;
+  } else if (tiles <= 512 && need > lds) {
+    const long room = tiles <= 256 ? kMostLds : 74 * 1024;
+    lds = (int)(need < room ? need : room);
   }
   const dim3 grid((unsigned)items * ceil_div(width, (GLU ? 8 : 16) * WC * NT));
-  hipLaunchKernelGGL((k_matvec<FMT, F32, GLU, WHOLE, kQuads>), grid, dim3(64 * WC * KS), lds, stream, a, NT, WC, KS, lds);
+  hipLaunchKernelGGL((k_matvec<FMT, F32, GLU, WHOLE, NQ>), grid, dim3(64 * WC * KS), lds, stream, a, NT, WC, KS, lds);
+}
+template <int FMT, bool F32, bool GLU, bool WHOLE>
+static void launch_one(const MatvecArgs& a, hipStream_t stream) {
+  if constexpr (F32) {                                // items of 4 rows, if that brings the sets of waves about
+    const int width = GLU ? a.p.N / 2 : a.p.N;
+    const long row = 3L * (2 * kChunkK * ceil_div(a.p.K, kChunkK) + 16);
+    if (a.p.M > 4 && row * (a.p.M < 8 ? a.p.M : 8) > kMostLds && 4 * row <= kMostLds &&
+        (long)ceil_div(width, GLU ? 32 : 64) * max_tiles(a.p, 4) <= 256) {
+      launch_rows<FMT, F32, GLU, WHOLE, 1>(a, stream);
+      return;
+    }
+  }
+  launch_rows<FMT, F32, GLU, WHOLE, kQuads>(a, stream);
 }
 template <int FMT, bool F32, bool GLU>
 static void launch_whole(const MatvecArgs& a, hipStream_t stream) {

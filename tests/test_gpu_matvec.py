@@ -138,6 +138,19 @@ def test_larger_calls(gpu_lib, G, M, N, K, kind, glu, fmt, dtype):
            glu=gpu_lib.Config(cap=7.0) if glu else None)
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("G,M,N,K,kind,glu,dtype", [
+    # long rows in few groups: items of 4 fp32 rows in two and four sets of waves, two sets of 4 waves
+    (1, 8, 4608, 3328, "even", False, "f32"), (1, 8, 4608, 3328, "even", True, "f32"), (1, 6, 600, 4608, "even", True, "f32"),
+    (2, 9, 1100, 3360, "uneven", False, "f32"), (1, 8, 4600, 5120, "even", False, "bf16"), (1, 7, 4500, 5216, "even", True, "bf16"),
+    # what x needs of LDS, in one panel and in several
+    (2, 16, 4608, 1056, "even", False, "f32"), (1, 8, 16384, 3328, "even", False, "f32"), (3, 16, 5000, 1280, "uneven", True, "f32"),
+])
+def test_few_rows_of_long_groups(gpu_lib, G, M, N, K, kind, glu, dtype, fmt):
+    _check(gpu_lib, np.random.default_rng(G * 7919 + M * 31 + N + K), fmt, dtype, "f32", G, M, N, K, kind,
+           glu=gpu_lib.Config(cap=7.0) if glu else None)
+
+
 @pytest.mark.parametrize("cap_form", [0, 1, 2, 3])
 @pytest.mark.parametrize("dtype,out_dtype", [("bf16", "f32"), ("f32", "bf16")])
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
