@@ -351,15 +351,18 @@ static void launch_fmt(const MatvecArgs& a, hipStream_t stream) {
 // By the mean group, and by tiles of 64 columns of 16 rows (fewer leave CUs idle
 // there).  us, quads / wide, 4608 x 4608 NVFP4 bf16: 64 rows of one group 24.8/29.6
 // (360 tiles), 96 of 8 groups 47.0/44.1 (1008), 16384 columns 16 rows 21.9/30.0
-// (512), 32 rows 30.2/30.1 (768), 64 rows 55.9/40.7.  384 groups of 4608 x 2304,
-// mean 1.3, 4, 6, 8, 12 rows: MXFP4 bf16 295/-, 415/407, -, 550/459, 714/520;
-// fp32 333/293, 548/431, 705/495, -, 1219/619; NVFP4 fp32 370/386 (1.3), 591/553
-// (4), bf16 605/521 (8), 788/590 (12), gate/up with SwiGLU 580/596 (1.3), 823/801 (4).
+// (512), 32 rows 30.2/30.1 (768), 64 rows 55.9/40.7.  384 groups, mean 1.3, 2.7, 4, 5
+// rows: 4608 x 2304 NVFP4 bf16 285/312, 418/435, 419/428, 453/438, fp32 344/373,
+// 480/491, 576/512, 650/534; MXFP4 bf16 254/251, 370/369, 376/355, 405/367, fp32
+// 317/284, 443/375, 537/405, 606/428 (0.7: 216/195).  4608 x 4608 with SwiGLU:
+// NVFP4 bf16 514/565, 709/748, 762/768, 817/792, fp32 681/716, 953/944, 1128/992,
+// 1276/1029; MXFP4 bf16 504/501, 669/663, 720/680, 771/706, fp32 633/561, 905/742.
 static bool wide_rows(const MatvecArgs& a) {
   const long tiles = (long)max_tiles(a.p, 16) * ceil_div(a.swiglu ? a.p.N / 2 : a.p.N, a.swiglu ? 32 : 64);
   const long M = a.p.M, G = a.p.G;
   if (tiles < 768) return false;
-  return a.dtype == 1 ? (a.fmt == 4 ? 2 * M > G : M > 2 * G) : M > 3 * G;
+  if (a.fmt == 4) return a.dtype == 1 ? 2 * M > G : M > G;
+  return a.dtype == 1 ? M > 2 * G : M > 4 * G;
 }
 
 int launch_group_matvec(const MatvecArgs& a, hipStream_t stream) {
