@@ -131,8 +131,14 @@ def check_arch(arch: str) -> int:
     return load().moe_check_arch(arch.encode())
 
 
+class _Referenced:
+    """Room for Config.ref's structure beside the fields: vars(), copies and
+    pickles hold the fields alone."""
+    __slots__ = ("_by_ref",)
+
+
 @dataclass
-class Config:
+class Config(_Referenced):
     hidden: int = 4608
     ffn: int = 2304
     num_experts: int = 384
@@ -154,20 +160,20 @@ class Config:
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
-        self.__dict__.pop("_by_ref", None)
+        object.__setattr__(self, "_by_ref", None)
 
     def ref(self):
         """A reference to the C structure for a call, built again after a field
         was set (building it takes 1 us of a small call's 6)."""
-        by_ref = self.__dict__.get("_by_ref")
+        by_ref = getattr(self, "_by_ref", None)
         if by_ref is None:
             by_ref = ctypes.byref(self.c())
             if isinstance(self.act_gs_static, tuple):   # anything else could change unseen
-                self.__dict__["_by_ref"] = by_ref
+                object.__setattr__(self, "_by_ref", by_ref)
         return by_ref
 
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k != "_by_ref"}
+        return dict(self.__dict__)
 
     def c(self) -> CConfig:
         if self.fmt not in FMTS:

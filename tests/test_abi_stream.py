@@ -140,3 +140,27 @@ def test_forward_quantized_arguments(lib):
     nn = bse.workspace_size(nv)
     assert call(c=nv.c(), weights=wn, nb=nn, gs=None) == -1
     assert call(c=nv.c(), weights=wn, nb=nn, gs=AT(0x100002)) == -1
+
+
+def test_config_holds_its_fields_alone():
+    """The structure that a call took leaves no trace in the Config, its copies
+    and pickles, and follows the fields."""
+    import copy
+    import dataclasses
+    import pickle
+
+    import block_scaled_expert_amd as bse
+    cfg = bse.Config(top_k=4)
+    before = dict(vars(cfg))
+    assert cfg.ref()._obj.top_k == 4 and cfg.ref() is cfg.ref()
+    assert vars(cfg) == before and bse.Config(**vars(cfg)) == cfg == dataclasses.replace(cfg)
+    for twin in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg))):
+        assert twin == cfg
+        twin.top_k = 2
+        assert twin.ref()._obj.top_k == 2 and cfg.ref()._obj.top_k == 4
+    cfg.top_k = 3
+    assert cfg.ref()._obj.top_k == 3
+    cfg.act_gs_static = [1.0, 1.0]
+    cfg.ref()
+    cfg.act_gs_static[0] = 2.0
+    assert cfg.ref()._obj.act_gs_static[0] == 2.0
