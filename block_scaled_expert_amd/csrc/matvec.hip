@@ -287,7 +287,11 @@ constexpr int kQuads = 2;
 //    more than 3 rows, 4 waves bring x in again for every tile (1536 rows down
 //    in fp32 624 us instead of 553, gate/up 882 instead of 842).  At 76 KiB only
 //    one workgroup with SwiGLU fits a CU: 64 tokens' gate/up 582 us instead of 551,
-//    with fp32 rows 767 instead of 686;
+//    with fp32 rows 767 instead of 686.
+//    Also where fp32 rows take several panels, unless most groups are empty and
+//    the others have a row each (16 rows of one group of 16384 x 4608 32.6 us
+//    instead of 40.0, 64 of 4 of 2048 x 2048 16.5 instead of 18.5; one token's
+//    gate/up in fp32 31.8 instead of 28.1);
 //  - up to 256, where all of x fits, two sets of 2 waves share the chunks, up to
 //    128 four sets: there are not enough columns to go round (4608 x 4608, one
 //    row: 8.7 us instead of 11.8; 16384 columns 12.9 instead of 13.7; 4 rows in
@@ -295,25 +299,26 @@ constexpr int kQuads = 2;
 //    waves where one workgroup fills a CU's LDS (13.3 instead of 28.0 as one item,
 //    25.4 in sets of 2);
 //  - up to 512 (256) otherwise, what x needs up to 74 (150) KiB, as two workgroups
-//    a CU (one) leave it: 8 fp32 rows, 16384 x 4608, 28.3 us instead of 32.0.
+//    of 4 waves a CU (one) leave it: 8 fp32 rows, 16384 x 4608, 28.3 us instead of 32.0.
 constexpr long kMostLds = 150 * 1024;
 template <int FMT, bool F32, bool GLU, bool WHOLE, int NQ>
 static void launch_rows(const MatvecArgs& a, hipStream_t stream) {
   const int width = GLU ? a.p.N / 2 : a.p.N, items = max_tiles(a.p, 4 * NQ), chunks = ceil_div(a.p.K, kChunkK);
   const long tiles = (long)ceil_div(width, GLU ? 32 : 64) * items;
-  int WC = tiles <= 10240 ? 4 : 8, KS = 1, lds = (WC == 8 ? 74 : 36) * 1024;
+  const int most = a.p.M < 4 * NQ ? a.p.M : 4 * NQ;   // rows of an item at most
+  const long need = (long)(F32 ? 3 : 1) * most * (2 * kChunkK * chunks + 16);
+  const bool panels = F32 && need > 36 * 1024 && 4L * a.p.M > a.p.G;
+  int WC = tiles > 10240 || panels ? 8 : 4, KS = 1, lds = (WC == 8 ? 74 : 36) * 1024;
   // tiles a workgroup takes in turn, so that there remain about 1024 workgroups (2 to 4 a CU)
   const long nt = tiles * 4 / WC / 1024;
   const int NT = (int)(nt < 1 ? 1 : nt > 4 ? 4 : nt);
-  const int most = a.p.M < 4 * NQ ? a.p.M : 4 * NQ;   // rows of an item at most
-  const long need = (long)(F32 ? 3 : 1) * most * (2 * kChunkK * chunks + 16);
   if (tiles <= 256 && need <= kMostLds && chunks > 1) {
     KS = tiles <= 128 && chunks > 3 ? 4 : 2;
     WC = KS == 2 && need > 74 * 1024 ? 4 : 2;         // one workgroup a CU: as many as tiles
     const int red = (KS - 1) * WC * NQ * 2048;
     lds = need > red ? (int)need : red;
   } else if (tiles <= 512 && need > lds) {
-    const long room = tiles <= 256 ? kMostLds : 74 * 1024;
+    const long room = tiles <= (WC == 8 ? 512 : 256) ? kMostLds : 74 * 1024;
     lds = (int)(need < room ? need : room);
   }
   const dim3 grid((unsigned)items * ceil_div(width, (GLU ? 8 : 16) * WC * NT));

@@ -206,8 +206,11 @@ template <int FMT, bool F32, bool GLU>
 static void launch_one(const MatvecArgs& a, hipStream_t stream) {
   const int width = GLU ? a.p.N / 2 : a.p.N, items = max_tiles(a.p, 16);
   const long tiles = (long)ceil_div(width, GLU ? 32 : 64) * items;
-  // 8 waves and 76 KiB where there are enough tiles; up to two tiles in turn
-  const int WC = tiles <= 2048 ? 4 : 8, lds = (WC == 8 ? 76 : 36) * 1024;
+  // 8 waves and 76 KiB where there are enough tiles, and for fp32 rows, whose panels
+  // 8 waves share (64 rows of 8 groups of 4608 x 2304 29.9 us, with 4 waves and 36
+  // KiB 49.5); else 4, and 76 KiB as long as every workgroup has a place (bf16, 4608
+  // x 4608 with SwiGLU: 42.4 instead of 44.4).  Up to two tiles in turn.
+  const int WC = F32 || tiles > 2048 ? 8 : 4, lds = (WC == 8 || tiles <= 1024 ? 76 : 36) * 1024;
   const int NT = tiles * 2 / WC / 1024 >= 2 ? 2 : 1;
   const dim3 grid((unsigned)items * ceil_div(width, (GLU ? 16 : 32) * WC * NT)), block(64 * WC);
   if (a.p.K % kChunkK == 0) hipLaunchKernelGGL((k_matvec_wide<FMT, F32, GLU, true>), grid, block, lds, stream, a, NT, WC, lds);
