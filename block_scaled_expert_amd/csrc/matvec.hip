@@ -17,7 +17,9 @@
 //    is done.  So lanes may hold codes of any row and block, as they were loaded,
 //    and an NVFP4 block's scale is applied to its 4 sums instead of its 16 codes
 //    (0.75 vector instructions a weight; widening and scaling each code for
-//    16x16x32 took 2, and 612 us where this took 556);
+//    16x16x32 took 2, and 612 us where this took 556).  Until then the codes are
+//    kept 2^-7 smaller (kSmaller), so that 16 products of 6 and the largest x stay
+//    in fp32's range; powers of two change no rounding above its least numbers;
 //  - scales are loaded four chunks at a time (Scales).
 // x, in bf16, waits in LDS; an fp32 x as three bf16 parts whose sum it is.
 // Products are exact and sums fp32; gs is applied to the sums.  A row's bits do
@@ -34,6 +36,9 @@
 namespace moe {
 
 namespace {
+
+// Of NVFP4's codes until the sums of a tile are done: 16 * 6 < 2^7.
+constexpr float kSmaller = 0x1p-7f;
 
 __device__ inline v4s lo4(v8s v) { return v4s{v[0], v[1], v[2], v[3]}; }
 __device__ inline v4s hi4(v8s v) { return v4s{v[4], v[5], v[6], v[7]}; }
@@ -156,7 +161,8 @@ __global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, in
       if (4 * k >= rows) continue;
       v[k] = lanes_by_8(acc[k], r);
       if constexpr (FMT == 1)
-        v[k] *= a.gs[(size_t)g * a.gs_stride + (half * width + min(n, width - 1)) / (p.N / a.gs_group)];
+        v[k] = v[k] * (1.0f / kSmaller) *
+               a.gs[(size_t)g * a.gs_stride + (half * width + min(n, width - 1)) / (p.N / a.gs_group)];
     }
     if constexpr (GLU) {                            // two tiles' worth of room: one barrier a tile
       if (half)
@@ -211,7 +217,7 @@ __global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, in
             scale[y] = FMT == 4 ? bits_f((s & 0xFFu) << 23)
                                 : e == 0 ? __builtin_amdgcn_cvt_f32_fp8(s, 0) : __builtin_amdgcn_cvt_f32_fp8(s, 1);
 #pragma unroll
-            for (int q = 0; q < 2; q++) w[y][q] = widen(ring[j].q[y][2 * e + q], FMT == 4 ? scale[y] : 1.0f);
+            for (int q = 0; q < 2; q++) w[y][q] = widen(ring[j].q[y][2 * e + q], FMT == 4 ? scale[y] : kSmaller);
           }
 #pragma unroll
           for (int k = 0; k < NQ; k++) {

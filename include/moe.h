@@ -367,7 +367,10 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
  * then [M][N/2].
  *  x [x_rows][K] bf16 or fp32 (x_dtype).  The weights' values enter exactly,
  *  products are exact, sums fp32, out is fp32 or bf16 (out_dtype, one
- *  rounding to nearest even).
+ *  rounding to nearest even).  NVFP4: what is summed is code * block scale *
+ *  x, and the fp32 scale gs is applied to the sum, which has to stay in fp32's
+ *  range before it as after (magnitudes of the terms that add up to less than
+ *  2^128 do); of sums below 2^-119, what lies under 2^-142 is lost.
  *  fmt: MOE_FMT_NVFP4 or MOE_FMT_MXFP4 (others: MOE_ERR_UNSUPPORTED_FORMAT).
  *  w [G][N][K/2], w_scales [G][N][K/16] (NVFP4) or [G][N][K/32] (MXFP4),
  *  canonical, as moe_encode_weights writes them.  NVFP4: the N rows of a
