@@ -177,6 +177,12 @@ struct Panels {
   }
 };
 
+// The capped SwiGLU, NaN kept: cap_swiglu's hard cap takes the cap instead.
+__device__ inline float glu_of(float g, float u, const MatvecArgs& a) {
+  const float h = cap_swiglu(g, u, a.cap_form, a.cap, 1.0f / a.cap);
+  return g == g && u == u ? h : g + u;
+}
+
 // More rows per group (matvec_wide.hip).
 int launch_matvec_wide(const MatvecArgs& a, hipStream_t stream);
 

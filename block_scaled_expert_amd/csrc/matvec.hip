@@ -177,7 +177,7 @@ __global__ __launch_bounds__(512) void k_matvec(MatvecArgs a, int NT, int WC, in
       const int m = 4 * k + b;
       if (m < rows) {
         float o = v[k];
-        if constexpr (GLU) o = cap_swiglu(o, up[t & 1][pair][k][lane], a.cap_form, a.cap, 1.0f / a.cap);
+        if constexpr (GLU) o = glu_of(o, up[t & 1][pair][k][lane], a);
         o = src[m] < 0 ? 0.0f : o;
         const size_t i = (size_t)(m0 + m) * width + n;
         if (p.out_f32) static_cast<float*>(p.out)[i] = o;

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(512) void k_matvec_wide(MatvecArgs a, int NT, int W
       for (int q = 0; q < 4; q++) {
         const int m = 4 * b + q;
         if (m >= rows) continue;
-        if constexpr (GLU) put(m, n, cap_swiglu(acc[0][q] * gs[0], acc[1][q] * gs[1], a.cap_form, a.cap, 1.0f / a.cap));
+        if constexpr (GLU) put(m, n, glu_of(acc[0][q] * gs[0], acc[1][q] * gs[1], a));
         else put(m, n, acc[h][q] * gs[0]);
       }
     }

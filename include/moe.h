@@ -379,7 +379,8 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
  *  canonical moe_expert_weights w13 with gs, gs_group 2, gs_stride 3; w2 with
  *  gs + 2, gs_group 1, gs_stride 3.  MXFP4 reads none of the three.  NaN
  *  scale bytes (E8M0 255, E4M3 0x7F and 0xFF; never written by the encoder)
- *  give NaN.
+ *  give NaN, with swiglu too: a NaN gate or up value makes NaN under every
+ *  cap (moe_cap_swiglu's hard cap puts the cap in its place).
  *  An MXFP4 weight of 2^128 and more (no finite weight is encoded as one) is
  *  infinite.  fp32 x enters as three bf16 parts, whole down to 2^-110; below,
  *  what lies under 2^-133 is dropped.

@@ -85,3 +85,30 @@ def test_nvfp4_least_rows(gpu_lib, gs, rows):
         # as above; and each rounding below the normal range is one of 2^-149, of sums that are kept 2^-7 smaller
         tol = 15 * 2.0 ** -23 * size + 15 * 2.0 ** -142 * 2 * gs + 2.0 ** -149
         assert (np.abs(got[a:b] - ref) <= tol).all(), i
+
+
+@pytest.mark.parametrize("cap_form", [0, 1, 2, 3])
+@pytest.mark.parametrize("rows", list(ROWS))
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_nan_under_every_cap(gpu_lib, fmt, dtype, rows, cap_form):
+    """A NaN scale byte of a gate or an up row makes its column of the group's rows
+    NaN, a NaN in x its row, whichever cap is taken."""
+    import torch
+    M, g = ROWS[rows], np.random.default_rng(5)
+    codes = g.integers(0, 256, (G, N, K // 2), dtype=np.uint8)
+    sc = g.integers(*((0x20, 0x50) if fmt == "nvfp4" else (119, 123)), (G, N, K // (16 if fmt == "nvfp4" else 32)), dtype=np.uint8)
+    nan = 0x7F if fmt == "nvfp4" else 255
+    sc[0, 37, 1] = nan                   # a gate row
+    sc[1, N // 2 + 5, 2] = nan           # an up row
+    v = g.standard_normal((M, K))
+    v[2, 11] = float("nan")
+    x, _ = _x(v, dtype)
+    off, out = _offsets(M), torch.empty((M, N // 2), device="cuda")
+    kw = dict(gs=torch.full((G,), 1e-2, device="cuda")) if fmt == "nvfp4" else {}
+    gpu_lib.group_matvec(fmt, x, to_dev(codes), to_dev(sc), to_dev(off), out, swiglu=gpu_lib.Config(cap_form=cap_form, cap=7.0), **kw)
+    want = np.zeros((M, N // 2), bool)
+    want[2] = True
+    want[:off[1], 37] = True
+    want[off[1]:, 5] = True
+    assert np.array_equal(out.isnan().cpu().numpy(), want)
