@@ -381,9 +381,11 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
  *  scale bytes (E8M0 255, E4M3 0x7F and 0xFF; never written by the encoder)
  *  give NaN, with swiglu too: a NaN gate or up value makes NaN under every
  *  cap (moe_cap_swiglu's hard cap puts the cap in its place).
- *  An MXFP4 weight of 2^128 and more (no finite weight is encoded as one) is
- *  infinite.  fp32 x enters as three bf16 parts, whole down to 2^-110; below,
- *  what lies under 2^-133 is dropped.
+ *  An MXFP4 weight of 2^128 and more (scale bytes 253 and 254; no finite
+ *  weight is encoded as one) is infinite; an fp32 x, whose lower parts may be
+ *  zero, gives infinity or NaN with it.
+ *  fp32 x enters as three bf16 parts, whole down to 2^-110; below, what lies
+ *  under 2^-133 is dropped.
  *  offsets [G+1] ascending, within [0, M] (values outside are clamped); a
  *  group may be empty.  out: rows in no group are not written.  A row whose
  *  source lies outside [0, x_rows) is zero.  out may not overlap the inputs.

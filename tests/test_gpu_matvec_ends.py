@@ -112,3 +112,26 @@ def test_nan_under_every_cap(gpu_lib, fmt, dtype, rows, cap_form):
     want[:off[1], 37] = True
     want[off[1]:, 5] = True
     assert np.array_equal(out.isnan().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("rows", list(ROWS))
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_mxfp4_weights_beyond_fp32(gpu_lib, dtype, rows):
+    """A weight of 2^128 and more (scale bytes 253 and 254) is infinite: its outputs
+    are infinite under bf16 rows; an fp32 row's parts may be zero, where infinity
+    gives NaN, so they are infinite or NaN.  Other outputs are not touched."""
+    import torch
+    M, g = ROWS[rows], np.random.default_rng(6)
+    codes = np.full((G, N, K // 2), 0x22, np.uint8)                        # 1.0
+    sc = np.full((G, N, K // 32), 127, np.uint8)
+    sc[0, 3], codes[0, 3, 5] = 254, 0x24                                   # 2^127 and one of 2^128
+    codes[0, 3, :5] = codes[0, 3, 6:] = 0
+    sc[1, 9], codes[1, 9] = 253, 0x77                                      # 6 * 2^126
+    x, xv = _x(np.abs(g.standard_normal((M, K))) + 0.5, dtype)
+    off, out = _offsets(M), torch.empty((M, N), device="cuda")
+    gpu_lib.group_matvec("mxfp4", x, to_dev(codes), to_dev(sc), to_dev(off), out)
+    got = out.cpu().numpy()
+    mine = np.zeros((M, N), bool)
+    mine[:off[1], 3] = mine[off[1]:, 9] = True
+    assert np.isfinite(got[~mine]).all()
+    assert (np.isposinf(got[mine]) if dtype == "bf16" else ~np.isfinite(got[mine])).all()
