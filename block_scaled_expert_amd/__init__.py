@@ -194,14 +194,15 @@ def _accessors():
     return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _stream(t=None) -> int:
-    """The current stream's handle; t, one of a call's tensors, must be on the
-    current device.  The raw accessors: building a Stream object takes 3 us, more
-    than everything else around a small call."""
+def _stream(*tensors) -> int:
+    """The current stream's handle; all of a call's tensors that are passed must
+    be on the current device (None: not given).  The raw accessors: building a
+    Stream object takes 3 us, more than everything else around a small call."""
     stream, device = _accessors()
     current = device()
-    if t is not None and t.get_device() != current:
-        raise ValueError(f"tensors must be on the current device ({current}), got one on {t.get_device()}")
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"tensors must be on the current device ({current}), got one on {t.get_device()}")
     return stream(current)
 
 
@@ -487,7 +488,8 @@ def group_matvec(fmt: str, x, w, w_scales, offsets, out, gs=None, gs_group: int 
                                 _ptr(w_scales, torch.uint8, (G, N, _scale_cols(fmt, K)), "w_scales"),
                                 _ptr(gs, torch.float32, None, "gs") if nv else None, gs_group, gs_stride, G, N, K,
                                 _ptr(offsets, torch.int32, (G + 1,), "offsets"), _dtype(out, "out"),
-                                _ptr(out, None, (M, N if swiglu is None else N // 2), "out"), _stream(x)),
+                                _ptr(out, None, (M, N if swiglu is None else N // 2), "out"),
+                                _stream(x, w, w_scales, offsets, out, gs if nv else None, row_ids)),
         "moe_group_matvec")
 
 
@@ -516,7 +518,9 @@ def norm_forward(x, weight, y=None, residual=None, res_out=None, rstd=None, eps:
                                 _ptr(residual, res_type, (T, cols), "residual"), T, cols,
                                 _ptr(weight, torch.float32, (cols,), "weight"), eps,
                                 _ptr(res_out, res_type, (T, cols), "res_out"), _ptr(y, x.dtype, (T, cols), "y"),
-                                _ptr(rstd, torch.float32, (T,), "rstd"), *enc, _stream(x)), "moe_norm_forward")
+                                _ptr(rstd, torch.float32, (T,), "rstd"), *enc,
+                                _stream(x, weight, y, residual, res_out, rstd, codes, scales, row_gs if enc[2] else None)),
+        "moe_norm_forward")
 
 
 def norm_workspace_size(T: int, cols: int) -> int:
@@ -543,7 +547,8 @@ def norm_backward(dy, res, weight, rstd, d_res, ws=None, d_res_out=None, dx=None
                                  _ptr(rstd, torch.float32, (T,), "rstd"), _ptr(d_res, res.dtype, (T, cols), "d_res"),
                                  _ptr(dx, dy.dtype, (T, cols), "dx"),
                                  _ptr(d_weight, torch.float32, (cols,), "d_weight"),
-                                 _ptr(ws, torch.uint8, None, "ws"), 0 if ws is None else ws.numel(), _stream(dy)),
+                                 _ptr(ws, torch.uint8, None, "ws"), 0 if ws is None else ws.numel(),
+                                 _stream(dy, res, weight, rstd, d_res, ws, d_res_out, dx, d_weight)),
         "moe_norm_backward")
 
 
@@ -570,7 +575,7 @@ def sort_rows(x, pair_pos, out) -> None:
     M = out.shape[0]
     _ok(load().moe_sort_rows(_dtype(x, "x"), _ptr(x, None, None, "x"), T, _slots(pair_pos, T), cols,
                              _ptr(pair_pos, torch.int32, None, "pair_pos"), M, _ptr(out, x.dtype, (M, cols), "out"),
-                             _stream(x)), "moe_sort_rows")
+                             _stream(x, pair_pos, out)), "moe_sort_rows")
 
 
 def sort_rows_backward(d_out, pair_pos, dx) -> None:
@@ -580,7 +585,8 @@ def sort_rows_backward(d_out, pair_pos, dx) -> None:
     M = d_out.shape[0]
     _ok(load().moe_sort_rows_backward(_dtype(dx, "dx"), _ptr(d_out, dx.dtype, (M, cols), "d_out"), M,
                                       _ptr(pair_pos, torch.int32, None, "pair_pos"), T, _slots(pair_pos, T), cols,
-                                      _ptr(dx, None, None, "dx"), _stream(dx)), "moe_sort_rows_backward")
+                                      _ptr(dx, None, None, "dx"), _stream(dx, pair_pos, d_out)),
+        "moe_sort_rows_backward")
 
 
 def combine_rows(y, pair_pos, topk_w, out) -> None:
@@ -593,7 +599,8 @@ def combine_rows(y, pair_pos, topk_w, out) -> None:
     _ok(load().moe_combine_rows(_dtype(y, "y"), _ptr(y, None, (M, cols), "y"), M,
                                 _ptr(pair_pos, torch.int32, None, "pair_pos"),
                                 _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols, _dtype(out, "out"),
-                                _ptr(out, None, None, "out"), _stream(out)), "moe_combine_rows")
+                                _ptr(out, None, None, "out"),
+                                _stream(out, y, pair_pos, topk_w)), "moe_combine_rows")
 
 
 def combine_rows_backward(d_out, y, pair_pos, topk_w, dy, d_topk_w=None) -> None:
@@ -610,7 +617,8 @@ def combine_rows_backward(d_out, y, pair_pos, topk_w, dy, d_topk_w=None) -> None
                                          _ptr(y, None, (M, cols), "y"), M, _ptr(pair_pos, torch.int32, None, "pair_pos"),
                                          _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols,
                                          _ptr(dy, rows.dtype, (M, cols), "dy"),
-                                         _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"), _stream(d_out)),
+                                         _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"),
+                                         _stream(d_out, y, pair_pos, topk_w, dy, d_topk_w)),
         "moe_combine_rows_backward")
 
 
@@ -684,8 +692,12 @@ def forward_quantized(cfg: Config, codes, scales, topk_ids, topk_w, weights, out
     quantize_act at site 0): codes, scales and, for NVFP4, row_gs."""
     import torch
     T = codes.shape[0]
-    H, k = cfg.hidden, cfg.top_k
-    cw = weights if isinstance(weights, CWeights) else weights_struct(cfg, weights)
+    H, k, nv = cfg.hidden, cfg.top_k, cfg.fmt == "nvfp4"
+    if isinstance(weights, CWeights):
+        cw, held = weights, ()                        # plain addresses
+    else:
+        cw = weights_struct(cfg, weights)
+        held = [weights[name] for name in ("w13", "w13_sc", "w2", "w2_sc") + (("gs",) if nv else ())]
     ev = None
     if events is not None:
         if len(events) != 2 * len(STAGES):
@@ -693,11 +705,13 @@ def forward_quantized(cfg: Config, codes, scales, topk_ids, topk_w, weights, out
         ev = (ctypes.c_void_p * len(events))(*[e.cuda_event if e is not None else None for e in events])
     _ok(load().moe_forward_quantized(cfg.ref(), _ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, H)), "codes"),
                                      _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, H)), "scales"),
-                                     _ptr(row_gs, torch.float32, (T,), "row_gs") if cfg.fmt == "nvfp4" else None, T,
+                                     _ptr(row_gs, torch.float32, (T,), "row_gs") if nv else None, T,
                                      _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
                                      _ptr(topk_w, torch.float32, (T, k), "topk_w"), ctypes.byref(cw),
                                      _ptr(out, torch.bfloat16, (T, H), "out"), _ptr(ws, torch.uint8, None, "ws"),
-                                     ws.numel(), _stream(codes), ev), "moe_forward_quantized")
+                                     ws.numel(),
+                                     _stream(codes, scales, topk_ids, topk_w, out, ws, row_gs if nv else None, *held), ev),
+        "moe_forward_quantized")
 
 
 def forward_noalloc(cfg: Config, x, topk_ids, topk_w, weights, out) -> None:
