@@ -68,7 +68,7 @@ def test_a_field_set_while_the_structure_is_built():
                 cfg.top_k = 5
             return str.__hash__(self)
 
-    cfg = bse.Config(fmt=Name("nvfp4"), top_k=4)
+    cfg = bse.Config(fmt=Name("nvfp4"), top_k=4, cap=1.2345)     # of no other test
     seen = []
     cfg.ref()
     assert len(seen) >= 2
