@@ -81,10 +81,13 @@ __device__ inline void encode_nv(const float* v, int c, float gs, bool zero_row,
 }
 
 // v[k] = v[k] r w[k] as XT holds it, r = rstd + rest.  With the squares summed in
-// 64 bits and the errors of the products carried along, the fp32 result is the
-// exact one's rounding: where it lies next to a bf16 step, and its code next to a
-// step of the format, both fall on the definition's side (16384 x 4608 to MXFP8:
-// no code off, where 20 to 70 were in plain fp32; the time is the memory's still).
+// 64 bits and the errors of the products carried along, what is rounded to fp32 is
+// within 2^-45 of the exact value (e is exact up to its last rounding, 2^-47 of p;
+// the sum of the errors likewise), as long as the errors themselves are above
+// fp32's least numbers.  Where y lies next to a bf16 step, and its code next to a
+// step of the format, both then fall on the definition's side (16384 x 4608 to
+// MXFP8: no code off, where 20 to 70 were in plain fp32; the time is the memory's
+// still).
 template <typename XT, int N>
 __device__ inline void normed(float (&v)[N], const float (&w)[N], float rstd, float rest) {
 #pragma clang fp contract(off)

@@ -404,7 +404,12 @@ int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, con
  * and, with cfg not NULL, the quantization of the normed rows.
  *   s = x + residual            (in fp32, rounded to res_dtype; x without residual)
  *   r = 1 / sqrt(mean over the row of s^2 + eps)   (squares summed in 64 bits)
- *   y = s r weight              (the exact value rounded to fp32, then to dtype)
+ *   y = s r weight              (rounded to fp32, then to dtype; see below)
+ *  y carries the errors of its products and of r: before the rounding to fp32
+ *  it is within 2^-45 of its size of the exact value, so it is that value's
+ *  rounding unless the value lies as near to a tie.  Where s r or y is below
+ *  2^-100, and in rows of a root mean square above 2^100, the carried errors
+ *  underflow: there the fp32 number is within 2^-21 of its size (2^-149 at least).
  *  x, y [T][cols] of dtype; residual and res_out [T][cols] of res_dtype, which
  *  is dtype or fp32 (fp32 x with a bf16 stream: MOE_ERR_INVALID_ARG); weight
  *  [cols] fp32; eps > 0, finite.  residual, res_out (s) and rstd (r, [T]

@@ -138,6 +138,29 @@ def test_norm_within_a_rounding(gpu_lib, T, cols, dtype, res):
     _close(y, exact, (half + HALF[dtype] * (1 + half)) * exact.abs() + TINY)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_where_the_carried_errors_underflow(gpu_lib, dtype):
+    """Rows whose root mean square is near fp32's largest number, where 1 / rms and
+    its remainder are subnormal, and elements far below their row's."""
+    import torch
+    T, cols = 4, 1000
+    x = _rand((T, cols), 10, "f32").clamp(-3, 3)
+    x[0] *= 2.0 ** 126
+    x[1] *= 2.0 ** 110
+    x[2, ::3] *= 2.0 ** -107
+    x[3, ::3] *= 2.0 ** -120
+    x = x.to(_dt(dtype))
+    w = 1.0 + 0.3 * _rand((cols,), 11, "f32")
+    y, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+    gpu_lib.norm_forward(x, w, y, rstd=rstd, eps=1e-6)
+    want = (x.double().square().mean(1) + float(torch.tensor(1e-6))).rsqrt()
+    _close(rstd, want, U * (1 + 2.0 ** -20) * want + 2.0 ** -150)
+    exact = x.double() * want[:, None] * w.double()
+    # rstd as stored is off by U and half of 2^-149; two products and the sum of the rest
+    rel = 4 * U + 2.0 ** -150 / want[:, None]
+    _close(y, exact, (rel + HALF[dtype] * (1 + rel)) * exact.abs() + TINY)
+
+
 @pytest.mark.parametrize("fmt,act_gs", [("mxfp8", 0), ("mxfp4", 0), ("nvfp4", 0), ("nvfp4", 2)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("cols", [96, 2048, 4608])
