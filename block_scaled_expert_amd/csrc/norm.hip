@@ -340,19 +340,26 @@ int gradient_groups(int T, int cols) {
 }
 int partial_pitch(int cols) { return (int)align_up(cols, 8); }
 
+// Pieces of a thread by waves (gradient_waves, row_pieces): up to 4 waves 1 to 3,
+// 5 to 8 waves 3, above 2, 3, 4 or 8.
 template <typename XT, typename RT, bool FULL, bool NT>
 void backward_ch(const NormGradArgs& a, int grid, hipStream_t s) {
-  const int waves = gradient_waves(a.cols);
+  const int waves = gradient_waves(a.cols), pieces = row_pieces(a.cols, waves);
+#define MOE_NORM_BACKWARD(CH, TB) \
+  hipLaunchKernelGGL((k_norm_backward<XT, RT, FULL, CH, TB, NT>), dim3(grid), dim3(64 * waves), 0, s, a)
   if (waves <= 4) {
-    MOE_ROW_PIECES(row_pieces(a.cols, waves),
-                   hipLaunchKernelGGL((k_norm_backward<XT, RT, FULL, CH, 256, NT>), dim3(grid), dim3(64 * waves), 0, s, a))
+    if (pieces == 1) MOE_NORM_BACKWARD(1, 256);
+    else if (pieces == 2) MOE_NORM_BACKWARD(2, 256);
+    else MOE_NORM_BACKWARD(3, 256);
   } else if (waves <= 8) {
-    MOE_ROW_PIECES(row_pieces(a.cols, waves),
-                   hipLaunchKernelGGL((k_norm_backward<XT, RT, FULL, CH, 512, NT>), dim3(grid), dim3(64 * waves), 0, s, a))
+    MOE_NORM_BACKWARD(3, 512);
   } else {
-    MOE_ROW_PIECES(row_pieces(a.cols, waves),
-                   hipLaunchKernelGGL((k_norm_backward<XT, RT, FULL, CH, 1024, NT>), dim3(grid), dim3(64 * waves), 0, s, a))
+    if (pieces == 2) MOE_NORM_BACKWARD(2, 1024);
+    else if (pieces == 3) MOE_NORM_BACKWARD(3, 1024);
+    else if (pieces == 4) MOE_NORM_BACKWARD(4, 1024);
+    else MOE_NORM_BACKWARD(8, 1024);
   }
+#undef MOE_NORM_BACKWARD
 }
 template <typename XT, typename RT>
 void backward_full(const NormGradArgs& a, bool full, int grid, hipStream_t s) {
