@@ -95,7 +95,7 @@ __device__ inline void normed(float (&v)[N], const float (&w)[N], float rstd, fl
   for (int k = 0; k < N; k++) {
     const float p = v[k] * rstd, e = fmaf(v[k], rest, fmaf(v[k], rstd, -p));
     const float q = p * w[k], y = q + fmaf(e, w[k], fmaf(p, w[k], -q));
-    v[k] = stored<XT>(y == y ? y : q);           // inf: q has it, the errors are NaN
+    v[k] = stored<XT>(y == y && q != 0.0f ? y : q);   // inf: q has it, the errors are NaN; zero: q has the sign
   }
 }
 

@@ -161,6 +161,24 @@ def test_norm_where_the_carried_errors_underflow(gpu_lib, dtype):
     _close(y, exact, (rel + HALF[dtype] * (1 + rel)) * exact.abs() + TINY)
 
 
+@pytest.mark.parametrize("dtype,res", TYPES)
+@pytest.mark.parametrize("cols", [264, 1003])
+def test_zeros_keep_their_sign(gpu_lib, cols, dtype, res):
+    """s r weight of a negative zero is a negative zero, and the other way round
+    under a negative weight."""
+    import torch
+    x = _rand((4, cols), 12, dtype)
+    x[:, ::3], x[:, 1::5], x[3] = -0.0, 0.0, -0.0
+    r = None if res == "none" else torch.where(x == 0, x, torch.zeros_like(x)).to(_dt(res))
+    w = 1.0 + 0.1 * _rand((cols,), 13, "f32")
+    w[::4] *= -1.0
+    y = torch.empty_like(x)
+    gpu_lib.norm_forward(x, w, y, residual=r)
+    zero = x == 0
+    assert (y[zero] == 0).all()
+    assert torch.equal(y.signbit()[zero], (x.signbit() ^ w.signbit())[zero])
+
+
 @pytest.mark.parametrize("fmt,act_gs", [("mxfp8", 0), ("mxfp4", 0), ("nvfp4", 0), ("nvfp4", 2)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("cols", [96, 2048, 4608])
