@@ -11,7 +11,8 @@ the router's balance loss with its gradient, the residual norm with its
 gradient, moe_forward_quantized, and the sorted rows with their gradients).
 Tensors must be contiguous and on the current CUDA (HIP) device; apart from
 moe_forward_noalloc's fixed device array the library never allocates, so
-callers pass outputs and a workspace.
+callers pass outputs and a workspace.  The calls named from the norm on, and
+moe_group_matvec, refuse a tensor of another device.
 
 There is no fallback: if the built library is missing, load() raises.
 """
@@ -197,23 +198,27 @@ def _accessors():
     return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _stream(*tensors) -> int:
-    """The current stream's handle; all of a call's tensors that are passed must
-    be on the current device (None: not given).  The raw accessors: building a
-    Stream object takes 3 us, more than everything else around a small call."""
+def _device() -> int:
+    return _accessors()[1]()
+
+
+def _stream(on=None) -> int:
+    """The current stream's handle (on: the current device, where it is known).
+    The raw accessors: building a Stream object takes 3 us, more than everything
+    else around a small call."""
     stream, device = _accessors()
-    current = device()
-    for t in tensors:
-        if t is not None and t.get_device() != current:
-            raise ValueError(f"tensors must be on the current device ({current}), got one on {t.get_device()}")
-    return stream(current)
+    return stream(device() if on is None else on)
 
 
-def _ptr(t, dtype=None, shape=None, name="tensor"):
+def _ptr(t, dtype=None, shape=None, name="tensor", on=None):
+    """t's address; on: the device that it must be on (None: any GPU)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
+    if on is None:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+    elif t.get_device() != on:
+        raise ValueError(f"{name} must be on the current device ({on}), is on {t.get_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -475,6 +480,7 @@ def group_matvec(fmt: str, x, w, w_scales, offsets, out, gs=None, gs_group: int 
     [M].  swiglu: a Config whose capped SwiGLU is taken over [gate | up], out is
     then [M, N/2]."""
     import torch
+    on = _device()
     if fmt not in FMTS:
         raise ValueError(f"unknown format {fmt!r}")
     rows, K = x.shape
@@ -485,14 +491,13 @@ def group_matvec(fmt: str, x, w, w_scales, offsets, out, gs=None, gs_group: int 
         if gs_group < 1 or N % gs_group:
             raise ValueError("N must be a multiple of gs_group")
         _check_gs(gs, G * gs_group, gs_group, gs_stride)
-    _ok(load().moe_group_matvec(None if swiglu is None else swiglu.ref(), FMTS[fmt], _dtype(x, "x"), _ptr(x, None, None, "x"), rows,
-                                _ptr(row_ids, torch.int32, (M,), "row_ids"), id_div, M,
-                                _ptr(w, torch.uint8, (G, N, _code_cols(fmt, K)), "w"),
-                                _ptr(w_scales, torch.uint8, (G, N, _scale_cols(fmt, K)), "w_scales"),
-                                _ptr(gs, torch.float32, None, "gs") if nv else None, gs_group, gs_stride, G, N, K,
-                                _ptr(offsets, torch.int32, (G + 1,), "offsets"), _dtype(out, "out"),
-                                _ptr(out, None, (M, N if swiglu is None else N // 2), "out"),
-                                _stream(x, w, w_scales, offsets, out, gs if nv else None, row_ids)),
+    _ok(load().moe_group_matvec(None if swiglu is None else swiglu.ref(), FMTS[fmt], _dtype(x, "x"),
+                                _ptr(x, None, None, "x", on), rows, _ptr(row_ids, torch.int32, (M,), "row_ids", on), id_div, M,
+                                _ptr(w, torch.uint8, (G, N, _code_cols(fmt, K)), "w", on),
+                                _ptr(w_scales, torch.uint8, (G, N, _scale_cols(fmt, K)), "w_scales", on),
+                                _ptr(gs, torch.float32, None, "gs", on) if nv else None, gs_group, gs_stride, G, N, K,
+                                _ptr(offsets, torch.int32, (G + 1,), "offsets", on), _dtype(out, "out"),
+                                _ptr(out, None, (M, N if swiglu is None else N // 2), "out", on), _stream(on)),
         "moe_group_matvec")
 
 
@@ -504,6 +509,7 @@ def norm_forward(x, weight, y=None, residual=None, res_out=None, rstd=None, eps:
     x, y [T, cols] bf16 or fp32; residual, res_out [T, cols] of x's type or
     fp32; weight [cols] and rstd [T] fp32.  Without cfg no codes are written."""
     import torch
+    on = _device()
     if isinstance(cfg, str):
         cfg = _default_config(cfg)[0]
     T, cols = x.shape
@@ -511,18 +517,17 @@ def norm_forward(x, weight, y=None, residual=None, res_out=None, rstd=None, eps:
     res_type = None if res is None else res.dtype
     enc = (None, None, None)
     if cfg is not None:
-        enc = (_ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, cols)), "codes"),
-               _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, cols)), "scales"),
-               _ptr(row_gs, torch.float32, (T,), "row_gs") if cfg.fmt == "nvfp4" else None)
+        enc = (_ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, cols)), "codes", on),
+               _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, cols)), "scales", on),
+               _ptr(row_gs, torch.float32, (T,), "row_gs", on) if cfg.fmt == "nvfp4" else None)
     elif codes is not None or scales is not None or row_gs is not None:
         raise ValueError("codes, scales and row_gs need cfg")
-    _ok(load().moe_norm_forward(None if cfg is None else cfg.ref(), _dtype(x, "x"), _ptr(x, None, None, "x"),
+    _ok(load().moe_norm_forward(None if cfg is None else cfg.ref(), _dtype(x, "x"), _ptr(x, None, None, "x", on),
                                 _dtype(x if res is None else res, "residual"),
-                                _ptr(residual, res_type, (T, cols), "residual"), T, cols,
-                                _ptr(weight, torch.float32, (cols,), "weight"), eps,
-                                _ptr(res_out, res_type, (T, cols), "res_out"), _ptr(y, x.dtype, (T, cols), "y"),
-                                _ptr(rstd, torch.float32, (T,), "rstd"), *enc,
-                                _stream(x, weight, y, residual, res_out, rstd, codes, scales, row_gs if enc[2] else None)),
+                                _ptr(residual, res_type, (T, cols), "residual", on), T, cols,
+                                _ptr(weight, torch.float32, (cols,), "weight", on), eps,
+                                _ptr(res_out, res_type, (T, cols), "res_out", on), _ptr(y, x.dtype, (T, cols), "y", on),
+                                _ptr(rstd, torch.float32, (T,), "rstd", on), *enc, _stream(on)),
         "moe_norm_forward")
 
 
@@ -543,15 +548,15 @@ def norm_backward(dy, res, weight, rstd, d_res, ws=None, d_res_out=None, dx=None
     added: the gradient of the residual and of x.  dx: the same in dy's type.
     d_weight [cols] fp32 needs ws: norm_workspace(T, cols)."""
     import torch
+    on = _device()
     T, cols = dy.shape
-    _ok(load().moe_norm_backward(_dtype(dy, "dy"), _ptr(dy, None, None, "dy"), _dtype(res, "res"),
-                                 _ptr(res, None, (T, cols), "res"), _ptr(d_res_out, res.dtype, (T, cols), "d_res_out"),
-                                 T, cols, _ptr(weight, torch.float32, (cols,), "weight"),
-                                 _ptr(rstd, torch.float32, (T,), "rstd"), _ptr(d_res, res.dtype, (T, cols), "d_res"),
-                                 _ptr(dx, dy.dtype, (T, cols), "dx"),
-                                 _ptr(d_weight, torch.float32, (cols,), "d_weight"),
-                                 _ptr(ws, torch.uint8, None, "ws"), 0 if ws is None else ws.numel(),
-                                 _stream(dy, res, weight, rstd, d_res, ws, d_res_out, dx, d_weight)),
+    _ok(load().moe_norm_backward(_dtype(dy, "dy"), _ptr(dy, None, None, "dy", on), _dtype(res, "res"),
+                                 _ptr(res, None, (T, cols), "res", on), _ptr(d_res_out, res.dtype, (T, cols), "d_res_out", on),
+                                 T, cols, _ptr(weight, torch.float32, (cols,), "weight", on),
+                                 _ptr(rstd, torch.float32, (T,), "rstd", on), _ptr(d_res, res.dtype, (T, cols), "d_res", on),
+                                 _ptr(dx, dy.dtype, (T, cols), "dx", on),
+                                 _ptr(d_weight, torch.float32, (cols,), "d_weight", on),
+                                 _ptr(ws, torch.uint8, None, "ws", on), 0 if ws is None else ws.numel(), _stream(on)),
         "moe_norm_backward")
 
 
@@ -574,22 +579,23 @@ def sort_rows(x, pair_pos, out) -> None:
     """out[pair_pos[t, j]] = x[t] for the local pairs (pair_pos: dispatch's,
     int32 [T * top_k]).  x [T, cols] and out [M, cols] of one type, bf16 or fp32."""
     import torch
+    on = _device()
     T, cols = x.shape
     M = out.shape[0]
-    _ok(load().moe_sort_rows(_dtype(x, "x"), _ptr(x, None, None, "x"), T, _slots(pair_pos, T), cols,
-                             _ptr(pair_pos, torch.int32, None, "pair_pos"), M, _ptr(out, x.dtype, (M, cols), "out"),
-                             _stream(x, pair_pos, out)), "moe_sort_rows")
+    _ok(load().moe_sort_rows(_dtype(x, "x"), _ptr(x, None, None, "x", on), T, _slots(pair_pos, T), cols,
+                             _ptr(pair_pos, torch.int32, None, "pair_pos", on), M, _ptr(out, x.dtype, (M, cols), "out", on),
+                             _stream(on)), "moe_sort_rows")
 
 
 def sort_rows_backward(d_out, pair_pos, dx) -> None:
     """dx[t] = sum over the local pairs of d_out[pair_pos[t, j]]: sort_rows' gradient."""
     import torch
+    on = _device()
     T, cols = dx.shape
     M = d_out.shape[0]
-    _ok(load().moe_sort_rows_backward(_dtype(dx, "dx"), _ptr(d_out, dx.dtype, (M, cols), "d_out"), M,
-                                      _ptr(pair_pos, torch.int32, None, "pair_pos"), T, _slots(pair_pos, T), cols,
-                                      _ptr(dx, None, None, "dx"), _stream(dx, pair_pos, d_out)),
-        "moe_sort_rows_backward")
+    _ok(load().moe_sort_rows_backward(_dtype(dx, "dx"), _ptr(d_out, dx.dtype, (M, cols), "d_out", on), M,
+                                      _ptr(pair_pos, torch.int32, None, "pair_pos", on), T, _slots(pair_pos, T), cols,
+                                      _ptr(dx, None, None, "dx", on), _stream(on)), "moe_sort_rows_backward")
 
 
 def combine_rows(y, pair_pos, topk_w, out) -> None:
@@ -597,31 +603,31 @@ def combine_rows(y, pair_pos, topk_w, out) -> None:
     (topk_w fp32 [T, top_k]; None: all 1).  y [M, cols], out [T, cols], each
     bf16 or fp32."""
     import torch
+    on = _device()
     T, cols = out.shape
     M, k = y.shape[0], _slots(pair_pos, T)
-    _ok(load().moe_combine_rows(_dtype(y, "y"), _ptr(y, None, (M, cols), "y"), M,
-                                _ptr(pair_pos, torch.int32, None, "pair_pos"),
-                                _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols, _dtype(out, "out"),
-                                _ptr(out, None, None, "out"),
-                                _stream(out, y, pair_pos, topk_w)), "moe_combine_rows")
+    _ok(load().moe_combine_rows(_dtype(y, "y"), _ptr(y, None, (M, cols), "y", on), M,
+                                _ptr(pair_pos, torch.int32, None, "pair_pos", on),
+                                _ptr(topk_w, torch.float32, (T, k), "topk_w", on), T, k, cols, _dtype(out, "out"),
+                                _ptr(out, None, None, "out", on), _stream(on)), "moe_combine_rows")
 
 
 def combine_rows_backward(d_out, y, pair_pos, topk_w, dy, d_topk_w=None) -> None:
     """combine_rows' gradients: dy [M, cols] (y's type; may be y) and d_topk_w
     [T, top_k] fp32, either of them None.  y may be None where d_topk_w is."""
     import torch
+    on = _device()
     T, cols = d_out.shape
     k = _slots(pair_pos, T)
     rows = y if y is not None else dy
     if rows is None:
         raise ValueError("dy or y must be given")
     M = rows.shape[0]
-    _ok(load().moe_combine_rows_backward(_dtype(d_out, "d_out"), _ptr(d_out, None, None, "d_out"), _dtype(rows, "y"),
-                                         _ptr(y, None, (M, cols), "y"), M, _ptr(pair_pos, torch.int32, None, "pair_pos"),
-                                         _ptr(topk_w, torch.float32, (T, k), "topk_w"), T, k, cols,
-                                         _ptr(dy, rows.dtype, (M, cols), "dy"),
-                                         _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w"),
-                                         _stream(d_out, y, pair_pos, topk_w, dy, d_topk_w)),
+    _ok(load().moe_combine_rows_backward(_dtype(d_out, "d_out"), _ptr(d_out, None, None, "d_out", on), _dtype(rows, "y"),
+                                         _ptr(y, None, (M, cols), "y", on), M, _ptr(pair_pos, torch.int32, None, "pair_pos", on),
+                                         _ptr(topk_w, torch.float32, (T, k), "topk_w", on), T, k, cols,
+                                         _ptr(dy, rows.dtype, (M, cols), "dy", on),
+                                         _ptr(d_topk_w, torch.float32, (T, k), "d_topk_w", on), _stream(on)),
         "moe_combine_rows_backward")
 
 
@@ -637,9 +643,10 @@ def dispatch(cfg: Config, topk_ids, expert_offsets, sorted_pairs=None, pair_pos=
                             _ptr(ws, torch.uint8, None, "ws"), ws.numel(), _stream()), "moe_dispatch")
 
 
-def weights_struct(cfg: Config, w: dict) -> CWeights:
+def weights_struct(cfg: Config, w: dict, on=None) -> CWeights:
     """w: dict of device tensors w13, w13_sc, w2, w2_sc (uint8), gs (fp32,
-    NVFP4) and optionally layout (LAYOUT_CANONICAL by default)."""
+    NVFP4) and optionally layout (LAYOUT_CANONICAL by default).  on: the device
+    that they must be on (None: any GPU)."""
     import torch
     H, F, n = cfg.hidden, cfg.ffn, cfg.num_local
     nv = cfg.fmt == "nvfp4"
@@ -647,8 +654,8 @@ def weights_struct(cfg: Config, w: dict) -> CWeights:
         "w13": (n, 2 * F, _code_cols(cfg.fmt, H)), "w13_sc": (n, 2 * F, _scale_cols(cfg.fmt, H)),
         "w2": (n, H, _code_cols(cfg.fmt, F)), "w2_sc": (n, H, _scale_cols(cfg.fmt, F)),
     }
-    ptrs = {k: _ptr(w[k], torch.uint8, s, k) for k, s in shapes.items()}
-    gs = _ptr(w["gs"], torch.float32, (n, 3), "gs") if nv else None
+    ptrs = {k: _ptr(w[k], torch.uint8, s, k, on) for k, s in shapes.items()}
+    gs = _ptr(w["gs"], torch.float32, (n, 3), "gs", on) if nv else None
     return CWeights(ptrs["w13"], ptrs["w13_sc"], ptrs["w2"], ptrs["w2_sc"], gs, int(w.get("layout", LAYOUT_CANONICAL)))
 
 
@@ -694,26 +701,22 @@ def forward_quantized(cfg: Config, codes, scales, topk_ids, topk_w, weights, out
     """forward on tokens quantized already (norm_forward with cfg, or
     quantize_act at site 0): codes, scales and, for NVFP4, row_gs."""
     import torch
+    on = _device()
     T = codes.shape[0]
     H, k, nv = cfg.hidden, cfg.top_k, cfg.fmt == "nvfp4"
-    if isinstance(weights, CWeights):
-        cw, held = weights, ()                        # plain addresses
-    else:
-        cw = weights_struct(cfg, weights)
-        held = [weights[name] for name in ("w13", "w13_sc", "w2", "w2_sc") + (("gs",) if nv else ())]
+    cw = weights if isinstance(weights, CWeights) else weights_struct(cfg, weights, on)   # CWeights: plain addresses
     ev = None
     if events is not None:
         if len(events) != 2 * len(STAGES):
             raise ValueError("events must hold 2 per stage")
         ev = (ctypes.c_void_p * len(events))(*[e.cuda_event if e is not None else None for e in events])
-    _ok(load().moe_forward_quantized(cfg.ref(), _ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, H)), "codes"),
-                                     _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, H)), "scales"),
-                                     _ptr(row_gs, torch.float32, (T,), "row_gs") if nv else None, T,
-                                     _ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
-                                     _ptr(topk_w, torch.float32, (T, k), "topk_w"), ctypes.byref(cw),
-                                     _ptr(out, torch.bfloat16, (T, H), "out"), _ptr(ws, torch.uint8, None, "ws"),
-                                     ws.numel(),
-                                     _stream(codes, scales, topk_ids, topk_w, out, ws, row_gs if nv else None, *held), ev),
+    _ok(load().moe_forward_quantized(cfg.ref(), _ptr(codes, torch.uint8, (T, _code_cols(cfg.fmt, H)), "codes", on),
+                                     _ptr(scales, torch.uint8, (T, _scale_cols(cfg.fmt, H)), "scales", on),
+                                     _ptr(row_gs, torch.float32, (T,), "row_gs", on) if nv else None, T,
+                                     _ptr(topk_ids, torch.int32, (T, k), "topk_ids", on),
+                                     _ptr(topk_w, torch.float32, (T, k), "topk_w", on), ctypes.byref(cw),
+                                     _ptr(out, torch.bfloat16, (T, H), "out", on), _ptr(ws, torch.uint8, None, "ws", on),
+                                     ws.numel(), _stream(on), ev),
         "moe_forward_quantized")
 
 
