@@ -13,8 +13,13 @@
 // registers from its only load to its stores.  Sums are taken in a fixed order
 // (lane, wave, workgroup; dw: a workgroup's rows, then the workgroups), those of
 // squares in 64 bits, the others in fp32.  Measured, 16384 x 4608 (TB/s of what
-// has to move): bf16 with MXFP8 codes 113 us (6.0), bf16 x and an fp32 stream
-// 162 (5.6), its gradient 221 (5.5) and 4.1 for dw; 64 rows with codes 4.0.
+// has to move): bf16 with MXFP8 codes 113 us (6.0), MXFP4 109 (5.9), NVFP4 110
+// (5.9), bf16 x and an fp32 stream 162 (5.6), its gradient 221 (5.5) and 4.1 for
+// dw; 64 rows with codes 4.0.  Wide rows: registers go to scratch in the gradient,
+// up to 72 bytes a lane above 6144 columns where x or the stream is fp32, up to 76
+// above 12288, 300 to 700 above 16384 and 1400 to 1900 above 32768, where the
+// forward has 76 to 192 (4000 x 16384 with an fp32 stream 148 and 215 us, 5.3 and
+// 4.9; 2000 x 32768 151 and 687, 5.2 and 1.5; 1000 x 65536 230 and 1066, 3.4 and 1.0).
 #include "operators.h"
 #include "quant_row.h"
 #include "row_io.h"

@@ -10,10 +10,15 @@
 // once, addressed by token (reading by expert row instead would fetch a token
 // k times).  A wavefront has one token, so positions and weights are uniform;
 // pairs elsewhere are skipped before any load.  Sums are fp32 in slot order.
-// Measured, 16384 tokens of 4608, 8 slots (TB/s of what has to move): all local in
-// bf16, sort, combine and both gradients 1300 us in all (5.1), combine's gradient
-// 500 (5.1); an eighth local with fp32 expert rows 332 to 380 in all (4.8 to 5.5).
-// 64 tokens 2.8 (sort) and 4.2 (combine of fp32 rows).
+// Measured, 16384 tokens of 4608, 8 slots, us (TB/s of what has to move): all local
+// in bf16, sort 282 (4.8), combine 235 (5.8), its gradients 504 (5.1), sort's 234
+// (5.8), the four in turn 1300 (5.1); with fp32 expert rows combine 492 (5.2), its
+// gradients 1000 (5.1), the four 2055; an eighth local with fp32 expert rows 54, 90
+// (5.0), 150 (5.0), 46, the four 326 to 385 on different machines (4.7 to 5.5).
+// 64 tokens: sort 2.8 us, combine of fp32 rows 4.2.  For 1024 and more tokens of rows
+// off 8 elements or 16 bytes and above 1031 columns, four slots do not fit the
+// registers that the combine's bound of 1024 threads leaves: 8 to 408 bytes a lane go
+// to scratch; above 32768 columns 40 to 1320 in any rows (its gradients 268 to 492).
 #include "operators.h"
 #include "row_io.h"
 
@@ -57,7 +62,9 @@ __global__ __launch_bounds__(1024) void k_sort_rows(RowsArgs a) {
     sp.template store<NT>(static_cast<T*>(a.rows_out) + (size_t)p.row(next_slot(m)) * a.cols, r);
 }
 
-// acc += the next n of the slots in m, whose loads go out together.
+// acc += the next n of the slots in m, whose loads go out together (at 3 and 4 pieces
+// of fp32 rows the compiler leaves fewer registers than four slots take, and fewer
+// are out at a time).
 template <int n, bool NT, typename YT, typename S>
 __device__ inline void add_slots(const RowsArgs& a, const S& sp, const Pairs& p, uint64_t& m, float (&acc)[S::N]) {
   typename S::template Raw<YT> r[n];
@@ -166,8 +173,10 @@ namespace {
 
 // Workgroups of the sort and of the combine: a whole row each for many tokens, so
 // that a row's positions are fetched once and there is more in flight behind them
-// (an eighth local 392 us in all, in runs 432; 8 fp32 rows a token 842, in runs
-// 1124); for few tokens a run of 8 columns a thread, so that there are more.
+// (16384 tokens of 4608, 8 slots, in whole rows and in runs: combine of bf16 rows
+// 235 and 241 us, of fp32 rows 492 and 515, with an eighth local 90 and 92; sort 282
+// and 286, its gradient 234 and 240); for few tokens a run of 8 columns a thread, so
+// that there are more.
 constexpr int kManyTokens = 1024;
 struct Shape {
   int waves, pieces, runs;

@@ -392,6 +392,10 @@ int moe_group_product(int32_t fmt, const uint8_t* a, const uint8_t* a_scales, in
  *  K a multiple of 32 up to 2^20, 1 <= N <= 2^20 (even with swiglu), 1 <= G
  *  <= 1024, M and x_rows at most 2^26, (G + M / 8) ceil(N / 64) at most
  *  2^22.  x, w and out 16-byte aligned, the other arrays 4.
+ *  The same call gives the same bits, and a row's do not depend on its group's
+ *  other rows.  Which kernel takes a call and how its sums are split follow the
+ *  formats, G, M, N and K: the same row in a call of other sizes may differ in
+ *  its last places.
  * No workspace; one launch.  Any number of rows is right; what it is made for
  * is groups of up to 8 or 16 (by the mean group), each further 8 or 16 read the
  * group's weights again. */
@@ -420,9 +424,10 @@ int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, con
  *  32; NVFP4 with MOE_ACT_GS_PER_TENSOR, whose scale needs every row first, is
  *  MOE_ERR_INVALID_ARG.  cfg NULL: the three are NULL.
  *  0 <= T <= 2^21, 1 <= cols <= 65536.  Arrays aligned to their elements; with
- *  cfg x, residual, res_out, y, weight and codes 16-byte aligned.  Rows of a
- *  multiple of 8 elements in 16-byte aligned arrays are read and written 16
- *  bytes at a time, others element by element.
+ *  cfg x, residual, res_out, y, weight and codes 16-byte aligned.  Rows are
+ *  read and written 16 bytes at a time, at any alignment of their elements, and
+ *  the cols % 8 elements behind the last whole 8 one by one; aligned to 16 bytes
+ *  no such access lies across two lines.
  * No workspace; one launch. */
 int moe_norm_forward(const moe_config* cfg, int32_t dtype, const void* x, int32_t res_dtype, const void* residual,
                      int32_t T, int32_t cols, const float* weight, float eps, void* res_out, void* y, float* rstd,
@@ -467,9 +472,8 @@ int moe_norm_backward(int32_t dtype, const void* dy, int32_t res_dtype, const vo
  *  not both; y may be NULL where d_topk_w is; dy may be y.  Outputs may not
  *  overlap the inputs otherwise.  d_topk_w is what moe_balance_backward takes.
  *  0 <= T <= 2^21, 1 <= top_k <= 32, 1 <= cols <= 65536, 0 <= M <= 2^26.
- *  Arrays aligned to their elements; rows of a multiple of 8 elements in
- *  16-byte aligned arrays are read and written 16 bytes at a time, others
- *  element by element.  No workspace; one launch each. */
+ *  Arrays aligned to their elements; rows are read and written as the norm's
+ *  are.  No workspace; one launch each. */
 int moe_sort_rows(int32_t dtype, const void* x, int32_t T, int32_t top_k, int32_t cols, const int32_t* pair_pos,
                   int32_t M, void* out, void* stream);
 int moe_sort_rows_backward(int32_t dtype, const void* d_out, int32_t M, const int32_t* pair_pos, int32_t T,
