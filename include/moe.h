@@ -413,7 +413,8 @@ int moe_group_matvec(const moe_config* swiglu, int32_t fmt, int32_t x_dtype, con
  *  it is within 2^-45 of its size of the exact value, so it is that value's
  *  rounding unless the value lies as near to a tie.  Where s r or y is below
  *  2^-100, and in rows of a root mean square above 2^100, the carried errors
- *  underflow: there the fp32 number is within 2^-21 of its size (2^-149 at least).
+ *  underflow: there s r and y are each an fp32 number within 2^-21 of its size
+ *  (2^-149 at least).
  *  x, y [T][cols] of dtype; residual and res_out [T][cols] of res_dtype, which
  *  is dtype or fp32 (fp32 x with a bf16 stream: MOE_ERR_INVALID_ARG); weight
  *  [cols] fp32; eps > 0, finite.  residual, res_out (s) and rstd (r, [T]
